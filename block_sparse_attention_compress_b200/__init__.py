@@ -16,11 +16,14 @@ LIB_PATH = os.path.join(_PKG, "libnsa.so")
 
 NSA_OK, NSA_ERR_INVALID_ARG, NSA_ERR_UNSUPPORTED, NSA_ERR_WORKSPACE, NSA_ERR_CUDA, NSA_ERR_TIMEOUT = range(6)
 NSA_CODE_CU_SEQLENS = 200   # status word: a variable-length call's cu_seqlens broke its rules
+NSA_CODE_CACHE = 201        # status word: a call on a paged cache skipped a token
 NSA_MODE_NSA, NSA_MODE_MOBA, NSA_MODE_DSA = 0, 1, 2
 NSA_MAP_TOUCH, NSA_MAP_CONTAINED, NSA_MAP_OVERLAP = 0, 1, 2
+NSA_CACHE_BF16, NSA_CACHE_INT4 = 0, 1
 
 EXPORTED = ("nsa_workspace_size", "nsa_compress", "nsa_compress_append", "nsa_compress_mlp",
             "nsa_compress_append_mlp", "nsa_forward", "nsa_forward_varlen",
+            "nsa_cache_append", "nsa_cache_read", "nsa_cache_attention", "nsa_cache_attention_workspace",
             "nsa_dsa_forward", "nsa_backward", "nsa_backward_ex", "nsa_decode",
             "nsa_forward_noalloc", "nsa_device_status", "nsa_device_status_noalloc", "nsa_selftest_wait_timeout",
             "nsa_status_string")
@@ -52,6 +55,28 @@ class NsaConfig(ctypes.Structure):
         ("w_cmp_k2", ctypes.c_void_p), ("w_cmp_v2", ctypes.c_void_p),
         ("b_cmp_k", ctypes.c_void_p), ("b_cmp_v", ctypes.c_void_p),
     ]
+
+
+class NsaCache(ctypes.Structure):
+    """Mirror of ``nsa_cache`` in include/nsa.h: a paged key/value cache."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("format", "batch", "h_kv", "d_k", "d_v", "page_size", "n_pages", "max_pages")] + \
+               [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "page_table", "status")]
+
+
+class NsaCacheAppendArgs(ctypes.Structure):
+    """Mirror of ``nsa_cache_append_args`` in include/nsa.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out", "seqlens", "cu_seqlens", "cos_sin")] + \
+               [(n, ctypes.c_int64) for n in ("k_stride", "v_stride", "q_stride")] + \
+               [(n, ctypes.c_int32) for n in ("n_new", "total_tokens", "n_positions", "rot_dim", "interleaved", "h_q")]
+
+
+class NsaCacheAttentionArgs(ctypes.Structure):
+    """Mirror of ``nsa_cache_attention_args`` in include/nsa.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("seqlens", "slopes", "lse", "workspace")] + \
+               [("workspace_bytes", ctypes.c_size_t), ("softmax_scale", ctypes.c_float),
+                ("softcap", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("n_new", "h_q", "max_seqlen", "window")]
 
 
 class NsaError(RuntimeError):
@@ -93,6 +118,15 @@ def load_library() -> ctypes.CDLL:
     lib.nsa_forward_varlen.restype = ctypes.c_int
     lib.nsa_forward_varlen.argtypes = [vp, vp, vp, vp, vp, i32, cfgp, vp, vp]
     lib.nsa_forward.restype = ctypes.c_int
+    cachep, attnp = ctypes.POINTER(NsaCache), ctypes.POINTER(NsaCacheAttentionArgs)
+    lib.nsa_cache_append.argtypes = [cachep, ctypes.POINTER(NsaCacheAppendArgs), vp]
+    lib.nsa_cache_append.restype = ctypes.c_int
+    lib.nsa_cache_read.argtypes = [cachep, vp, vp, i32, i32, vp, vp, vp]
+    lib.nsa_cache_read.restype = ctypes.c_int
+    lib.nsa_cache_attention.argtypes = [cachep, vp, attnp, vp, vp]
+    lib.nsa_cache_attention.restype = ctypes.c_int
+    lib.nsa_cache_attention_workspace.argtypes = [cachep, attnp]
+    lib.nsa_cache_attention_workspace.restype = sz
     lib.nsa_decode.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, cfgp, vp, vp]
     lib.nsa_decode.restype = ctypes.c_int
     lib.nsa_forward_noalloc.argtypes = [vp, vp, vp, vp, cfgp, vp, vp]
@@ -243,6 +277,31 @@ def nsa_decode(q, k_cache, v_cache, kc_cache, vc_cache, seqlens, max_seqlen: int
                                    _ptr(seqlens), int(max_seqlen), _ptr(gates), ctypes.byref(cfg), _ptr(out),
                                    _stream(stream, q))
     return _check(st, "nsa_decode") if check else st
+
+
+def nsa_cache_append(cache: NsaCache, args: NsaCacheAppendArgs, stream=None, check: bool = True) -> int:
+    """Write new tokens into a paged cache, keys rotated on the way (see include/nsa.h)."""
+    st = load_library().nsa_cache_append(ctypes.byref(cache), ctypes.byref(args), _stream(stream))
+    return _check(st, "nsa_cache_append") if check else st
+
+
+def nsa_cache_read(cache: NsaCache, seqlens, cu_seqlens, n_new: int, total_tokens: int, k_out, v_out, stream=None,
+                   check: bool = True) -> int:
+    """The last tokens of every sequence out of a paged cache as bf16 (see include/nsa.h)."""
+    st = load_library().nsa_cache_read(ctypes.byref(cache), _ptr(seqlens), _ptr(cu_seqlens), int(n_new),
+                                       int(total_tokens), _ptr(k_out), _ptr(v_out), _stream(stream, k_out))
+    return _check(st, "nsa_cache_read") if check else st
+
+
+def nsa_cache_attention(cache: NsaCache, q, args: NsaCacheAttentionArgs, out, stream=None, check: bool = True) -> int:
+    """Attention of the newest tokens over a paged cache (see include/nsa.h)."""
+    st = load_library().nsa_cache_attention(ctypes.byref(cache), _ptr(q), ctypes.byref(args), _ptr(out),
+                                            _stream(stream, q))
+    return _check(st, "nsa_cache_attention") if check else st
+
+
+def nsa_cache_attention_workspace(cache: NsaCache, args: NsaCacheAttentionArgs) -> int:
+    return int(load_library().nsa_cache_attention_workspace(ctypes.byref(cache), ctypes.byref(args)))
 
 
 def nsa_device_status(workspace, stream=None) -> tuple[int, int]:

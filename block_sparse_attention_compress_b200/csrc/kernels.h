@@ -201,6 +201,52 @@ cudaError_t launch_backward(const BwdArgs& a, cudaStream_t st);
 // K6: one decode step per sequence, all branches in one launch.
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
 
+// The paged cache (see nsa_cache in include/nsa.h).
+struct CacheArgs {
+  void* k;                      // bf16 [n_pages, page_size, h_kv, d], or codes [n_pages, h_kv, page_size, d / 2]
+  void* v;
+  void* k_scale;                // 4 bits: bf16 (s, z) [n_pages, h_kv, page_size, d / 32, 2]
+  void* v_scale;
+  const int32_t* page_table;    // [batch, max_pages]
+  int32_t* status;              // optional device word: kErrCache where a token was skipped
+  int batch, h_kv, dk, dv, page_size, n_pages, max_pages;
+  bool int4;
+};
+constexpr int kErrCache = 201;
+
+// The rows an append or a read works on: the last n_new tokens of every sequence, or packed by cu.
+struct RowsArgs {
+  const int32_t* seqlens;
+  const int32_t* cu;
+  int n_new, rows;
+};
+
+struct AppendArgs {
+  const void* k;
+  const void* v;
+  const void* q;                // optional queries, rotated into q_out
+  void* q_out;
+  const float* cos_sin;         // optional [n_positions, rot]
+  int64_t k_stride, v_stride, q_stride;
+  int n_positions, rot, interleaved, h_q;
+};
+cudaError_t launch_cache_append(const CacheArgs& c, const RowsArgs& r, const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheArgs& c, const RowsArgs& r, void* k_out, void* v_out, cudaStream_t st);
+
+struct CacheAttnArgs {
+  const void* q;                // [B, n_new, h_q, dk]
+  void* out;                    // [B, n_new, h_q, dv]
+  float* lse;                   // optional [B, n_new, h_q]
+  const int32_t* seqlens;
+  const float* slopes;          // optional [h_q]
+  void* workspace;
+  float scale, softcap;
+  int n_new, h_q, G, max_seqlen, window;
+};
+size_t cache_attn_workspace(const CacheArgs& c, const CacheAttnArgs& a);
+bool cache_attn_fits(const CacheArgs& c, const CacheAttnArgs& a);   // its blocks fit a grid
+cudaError_t launch_cache_attn(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t st);
+
 // Self-test of the bounded-wait path: one wait on an mbarrier that nothing arrives at,
 // which gives up after limit_ns and records `code` in *err.
 cudaError_t launch_wait_timeout(int* err, uint64_t limit_ns, int code, cudaStream_t st);

@@ -247,7 +247,8 @@ nsa_status nsa_device_status(const void* workspace, int32_t* code_out, void* str
   if (cudaStreamSynchronize(s) != cudaSuccess) return NSA_ERR_CUDA;
   if (cudaMemcpy(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return NSA_ERR_CUDA;
   if (code_out) *code_out = word;
-  return word == 0 ? NSA_OK : word == NSA_CODE_CU_SEQLENS ? NSA_ERR_INVALID_ARG : NSA_ERR_TIMEOUT;
+  if (word == 0) return NSA_OK;
+  return word == NSA_CODE_CU_SEQLENS || word == NSA_CODE_CACHE ? NSA_ERR_INVALID_ARG : NSA_ERR_TIMEOUT;
 }
 
 nsa_status nsa_selftest_wait_timeout(void* workspace, size_t workspace_bytes, uint32_t limit_us, void* stream) {

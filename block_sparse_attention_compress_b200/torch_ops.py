@@ -5,7 +5,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (NSA_MODE_MOBA, NSA_MODE_NSA, make_config, nsa_compress, nsa_decode, nsa_forward,
+from . import (NSA_CACHE_BF16, NSA_CACHE_INT4, NSA_MODE_MOBA, NSA_MODE_NSA, NsaCache, NsaCacheAppendArgs,
+               NsaCacheAttentionArgs, make_config, nsa_cache_append, nsa_cache_attention,
+               nsa_cache_attention_workspace, nsa_cache_read, nsa_compress, nsa_decode, nsa_forward,
                nsa_forward_varlen, nsa_workspace_size)
 
 
@@ -85,3 +87,197 @@ def compress_torch(x, w, l=32, s=16):
     if out.shape[1]:
         nsa_compress(x, w, out, l, s)
     return out
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+class KVCache:
+    """A paged key/value cache in bf16 or in 4 bits, with the three calls that work on it.
+
+    ``KVCache(batch, max_len, h_kv, d_k, d_v)`` allocates the pool (``fmt`` "bf16" or "int4"),
+    a status word and a page table that gives every sequence its own pages in order; a program
+    with its own page allocator passes ``n_pages`` and writes ``page_table`` [batch, max_pages]
+    (int32) itself.  ``from_pools`` takes existing bf16 pools, such as
+    nsa_decode's caches.  Lengths (``seqlens``, int32 [batch] on the device) always count the new
+    tokens.
+
+    A token that cannot be placed (page table entry, position or length out of range) is skipped,
+    and ``device_status()`` is then NSA_CODE_CACHE until ``status`` is zeroed."""
+
+    def __init__(self, batch, max_len, h_kv, d_k, d_v, *, fmt="bf16", page_size=64, n_pages=None, device="cuda"):
+        _need(fmt in ("bf16", "int4"), f"fmt is 'bf16' or 'int4', not {fmt!r}")
+        _need(min(batch, max_len, h_kv, d_k, d_v, page_size) >= 1, "sizes must be at least 1")
+        max_pages = -(-max_len // page_size)
+        n_pages = batch * max_pages if n_pages is None else n_pages
+        _need(n_pages >= 1, "n_pages must be at least 1")
+        bf, u8 = torch.bfloat16, torch.uint8
+        if fmt == "bf16":
+            pools = (torch.zeros((n_pages, page_size, h_kv, d_k), dtype=bf, device=device),
+                     torch.zeros((n_pages, page_size, h_kv, d_v), dtype=bf, device=device), None, None)
+        else:
+            _need(d_k % 32 == 0 and d_v % 32 == 0, "4 bits: head dims are multiples of 32")
+            pools = (torch.zeros((n_pages, h_kv, page_size, d_k // 2), dtype=u8, device=device),
+                     torch.zeros((n_pages, h_kv, page_size, d_v // 2), dtype=u8, device=device),
+                     torch.zeros((n_pages, h_kv, page_size, d_k // 32, 2), dtype=bf, device=device),
+                     torch.zeros((n_pages, h_kv, page_size, d_v // 32, 2), dtype=bf, device=device))
+        table = torch.arange(batch * max_pages, dtype=torch.int32, device=device).view(batch, max_pages)
+        self._set(fmt, batch, h_kv, d_k, d_v, page_size, pools, table)
+
+    @classmethod
+    def from_pools(cls, k, v, page_table):
+        """Over existing bf16 pools k [n_pages, page_size, h_kv, d_k], v [.., d_v] and an int32
+        page table [batch, max_pages] on the same device."""
+        _need(k.dim() == 4 and v.dim() == 4 and k.shape[:3] == v.shape[:3], "k and v: [n_pages, page_size, h_kv, d]")
+        _need(k.dtype == v.dtype == torch.bfloat16, "k and v must be bf16")
+        _need(page_table.dim() == 2 and page_table.dtype == torch.int32, "page_table: int32 [batch, max_pages]")
+        self = cls.__new__(cls)
+        self._set("bf16", page_table.shape[0], k.shape[2], k.shape[3], v.shape[3], k.shape[1], (k, v, None, None), page_table)
+        return self
+
+    def _set(self, fmt, batch, h_kv, d_k, d_v, page_size, pools, table):
+        self.fmt, self.batch, self.h_kv, self.d_k, self.d_v, self.page_size = fmt, batch, h_kv, d_k, d_v, page_size
+        self.k, self.v, self.k_scale, self.v_scale = pools
+        self.page_table = table
+        self.device = self.k.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        for t in (self.k, self.v, self.page_table):
+            _need(t.is_cuda and t.device == self.device and t.is_contiguous(), "pools and page table: contiguous, on one GPU")
+        p = lambda t: t.data_ptr() if t is not None else None
+        self.desc = NsaCache(format=NSA_CACHE_INT4 if fmt == "int4" else NSA_CACHE_BF16, batch=batch, h_kv=h_kv, d_k=d_k,
+                             d_v=d_v, page_size=page_size, n_pages=self.k.shape[0], max_pages=table.shape[1],
+                             k=p(self.k), v=p(self.v), k_scale=p(self.k_scale), v_scale=p(self.v_scale),
+                             page_table=p(table), status=p(self.status))
+
+    @property
+    def max_len(self):
+        return self.desc.max_pages * self.page_size
+
+    def device_status(self) -> int:
+        """The status word after a synchronised call: 0, or NSA_CODE_CACHE."""
+        return int(self.status.item())
+
+    def _lengths(self, seqlens, cu_seqlens):
+        for t, n, name in ((seqlens, self.batch, "seqlens"), (cu_seqlens, self.batch + 1, "cu_seqlens")):
+            if t is not None:
+                _need(t.dtype == torch.int32 and t.shape == (n,) and t.device == self.device and t.is_contiguous(),
+                      f"{name}: int32 [{n}] on {self.device}")
+
+    def _rows(self, x, heads, d, packed, name):
+        """Checks new rows [batch, n, heads, d] (packed: [total, heads, d]); the elements from one
+        token to the next.  Tokens may lie apart (a slice of a wider row), a token's heads not."""
+        lead = 1 if packed else 2
+        _need(x.dim() == lead + 2 and x.shape[-2:] == (heads, d) and (packed or x.shape[0] == self.batch),
+              f"{name}: {'[total' if packed else f'[{self.batch}, n'}, {heads}, {d}], not {tuple(x.shape)}")
+        _need(x.dtype == torch.bfloat16 and x.device == self.device, f"{name}: bf16 on {self.device}")
+        _need(x.stride(-1) == 1 and (heads == 1 or x.stride(-2) == d), f"{name}: heads and dims must be contiguous")
+        if x.shape[:-2].numel() <= 1:
+            return max(heads * d, 8)
+        step, n = x.stride(-3), x.shape[-3]
+        if not packed and x.shape[0] > 1:
+            if n == 1:
+                step = x.stride(0)
+            else:
+                _need(x.stride(0) == n * step, f"{name}: tokens must lie at one stride")
+        return step
+
+    def append(self, k, v, seqlens, *, cu_seqlens=None, cos_sin=None, interleaved=False, q=None, q_out=None, stream=None):
+        """Write new tokens: k [batch, n, h_kv, d_k] and v [batch, n, h_kv, d_v] are the last n of
+        each sequence's ``seqlens`` tokens; with cu_seqlens (int32 [batch + 1]) packed [total, ...].
+        cos_sin fp32 [positions, rot_dim] (cosines, then sines) rotates the keys by their
+        positions, and the queries q [.., h_q, d_k], which are returned (into q_out)."""
+        packed = cu_seqlens is not None
+        self._lengths(seqlens, cu_seqlens)
+        a = NsaCacheAppendArgs(seqlens=seqlens.data_ptr(), k=k.data_ptr(), v=v.data_ptr())
+        a.k_stride = self._rows(k, self.h_kv, self.d_k, packed, "k")
+        a.v_stride = self._rows(v, self.h_kv, self.d_v, packed, "v")
+        _need(k.shape[:-2] == v.shape[:-2], "k and v must hold the same tokens")
+        if packed:
+            a.cu_seqlens, a.total_tokens = cu_seqlens.data_ptr(), k.shape[0]
+        else:
+            a.n_new = k.shape[1]
+        if cos_sin is not None:
+            _need(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.device == self.device and
+                  cos_sin.is_contiguous(), f"cos_sin: contiguous fp32 [positions, rot_dim] on {self.device}")
+            a.cos_sin, a.n_positions, a.rot_dim = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+            a.interleaved = int(interleaved)
+        if q is not None:
+            a.q_stride = self._rows(q, q.shape[-2], self.d_k, packed, "q")
+            _need(q.shape[:-2] == k.shape[:-2], "q must hold the same tokens as k")
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.device == q.device and
+                  q_out.is_contiguous(), "q_out: contiguous, like q")
+            a.q, a.q_out, a.h_q = q.data_ptr(), q_out.data_ptr(), q.shape[-2]
+        if k.shape[:-2].numel():   # no tokens: nothing to do
+            with torch.cuda.device(self.device):
+                nsa_cache_append(self.desc, a, torch.cuda.current_stream() if stream is None else stream)
+        return q_out if q is not None else None
+
+    def read(self, seqlens, n=None, *, cu_seqlens=None, total=None, k_out=None, v_out=None, stream=None):
+        """The last n tokens of each sequence as contiguous bf16 (k [batch, n, h_kv, d_k], v), or,
+        with cu_seqlens, the last cu[b+1] - cu[b] of each, packed into ``total`` rows."""
+        packed = cu_seqlens is not None
+        self._lengths(seqlens, cu_seqlens)
+        _need(total is not None if packed else n is not None, "read takes n, or cu_seqlens and total")
+        lead = (int(total),) if packed else (self.batch, int(n))
+        _need(min(lead) >= 0, "read takes a number of tokens")
+        outs = []
+        for t, d, name in ((k_out, self.d_k, "k_out"), (v_out, self.d_v, "v_out")):
+            if t is None:
+                t = torch.empty((*lead, self.h_kv, d), dtype=torch.bfloat16, device=self.device)
+            _need(t.shape == (*lead, self.h_kv, d) and t.dtype == torch.bfloat16 and t.device == self.device and
+                  t.is_contiguous(), f"{name}: contiguous bf16 {(*lead, self.h_kv, d)} on {self.device}")
+            outs.append(t)
+        if outs[0].numel():
+            with torch.cuda.device(self.device):
+                nsa_cache_read(self.desc, seqlens, cu_seqlens, 0 if packed else lead[1], lead[0] if packed else 0, *outs,
+                               stream=torch.cuda.current_stream() if stream is None else stream)
+        return tuple(outs)
+
+    def attend(self, q, seqlens, max_seqlen=None, *, softmax_scale=0.0, softcap=0.0, slopes=None, window=0, out=None,
+               lse=None, workspace=None, stream=None):
+        """Attention of the newest tokens q [batch, n, h_q, d_k] (n = 1 .. 16; their keys and values
+        are in the cache) over the cache.  max_seqlen bounds seqlens (default: the capacity; the
+        nearer the bound, the better the work is split).  softcap caps the scores by tanh, slopes
+        (fp32 [h_q]) adds slope * (u - p), window (0: none) keeps the last tokens; lse (fp32
+        [batch, n, h_q]) receives the log-sum-exps.  The workspace is torch's unless one of
+        attend_workspace() bytes is given."""
+        self._lengths(seqlens, None)
+        _need(q.dim() == 4 and q.shape[0] == self.batch and q.shape[1] >= 1 and q.shape[3] == self.d_k and
+              q.dtype == torch.bfloat16 and q.device == self.device and q.is_contiguous(),
+              f"q: contiguous bf16 [{self.batch}, n, h_q, {self.d_k}] on {self.device}")
+        B, n, h_q, _ = q.shape
+        if out is None:
+            out = torch.empty((B, n, h_q, self.d_v), dtype=torch.bfloat16, device=self.device)
+        _need(out.shape == (B, n, h_q, self.d_v) and out.dtype == torch.bfloat16 and out.device == self.device and
+              out.is_contiguous(), "out: contiguous bf16 [batch, n, h_q, d_v]")
+        for t, shape, name in ((slopes, (h_q,), "slopes"), (lse, (B, n, h_q), "lse")):
+            _need(t is None or (t.shape == shape and t.dtype == torch.float32 and t.device == self.device and
+                                t.is_contiguous()), f"{name}: contiguous fp32 {shape} on {self.device}")
+        a = NsaCacheAttentionArgs(seqlens=seqlens.data_ptr(), softmax_scale=softmax_scale, softcap=softcap, n_new=n,
+                                  h_q=h_q, max_seqlen=self.max_len if max_seqlen is None else max_seqlen, window=window)
+        if slopes is not None:
+            a.slopes = slopes.data_ptr()
+        if lse is not None:
+            a.lse = lse.data_ptr()
+        if workspace is None:
+            need = nsa_cache_attention_workspace(self.desc, a)
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+                if stream is not None:   # torch must not hand it out again before that stream is done
+                    workspace.record_stream(torch.cuda.ExternalStream(stream, device=self.device)
+                                            if isinstance(stream, int) else stream)
+        if workspace is not None:
+            a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        with torch.cuda.device(self.device):
+            nsa_cache_attention(self.desc, q, a, out, torch.cuda.current_stream() if stream is None else stream)
+        return out
+
+    def attend_workspace(self, n, h_q, max_seqlen=None, window=0):
+        """Bytes of workspace attend() needs for n new tokens and h_q query heads."""
+        return nsa_cache_attention_workspace(
+            self.desc, NsaCacheAttentionArgs(n_new=n, h_q=h_q, window=window,
+                                             max_seqlen=self.max_len if max_seqlen is None else max_seqlen))

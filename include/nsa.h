@@ -350,6 +350,143 @@ NSA_API nsa_status nsa_decode(const void* q, const void* k_cache, const void* v_
                       void* out, void* stream);
 
 /*
+ * A paged key/value cache, in bf16 or in 4 bits, for the layers that attend to everything they
+ * hold (the pages' D1, "all history kept, none evicted"): full attention layers, and the
+ * generation stage of layers that select blocks in the prompt only.  Three calls work on it:
+ * nsa_cache_append writes new tokens (keys rotated by their position on the way),
+ * nsa_cache_attention lets new tokens attend to it, nsa_cache_read gives rows back as bf16.
+ *
+ *   format      nsa_cache_format.
+ *   batch       sequences B (1 .. 65535).  h_kv, d_k, d_v: KV heads (1 .. 65535) and head dims,
+ *               (d_k, d_v) in {(64,64), (128,128), (192,128)}.
+ *   page_size,  tokens per page, and pages in the pool; max_pages: pages per sequence.
+ *   n_pages,    page_size is a multiple of 16, or in bf16 any size when max_pages is 1;
+ *   max_pages   max_pages * page_size (a sequence's capacity) <= 2^30.
+ *   page_table  int32 [B, max_pages] device: position p of sequence b is place p % page_size
+ *               of page page_table[b][p / page_size].  Entries outside [0, n_pages) are never
+ *               followed: a token there is not written, reads back as zeros and is masked out
+ *               of the attention; the status word (below) tells of it.  Entries of pages that no
+ *               call touches may hold anything.
+ *   k, v        NSA_CACHE_BF16: bf16 [n_pages, page_size, h_kv, d].  A cache of nsa_decode
+ *               [B, L_max, h_kv, d] is such a pool: n_pages = B, page_size = L_max,
+ *               max_pages = 1, page_table[b] = b (or any smaller page that divides L_max).
+ *               NSA_CACHE_INT4: codes uint8 [n_pages, h_kv, page_size, d / 2].
+ *   k_scale,    NSA_CACHE_INT4: bf16 [n_pages, h_kv, page_size, d / 32, 2], (s, z) of each group
+ *   v_scale     of 32 values; NULL with NSA_CACHE_BF16.
+ *   status      optional device word, 4-byte aligned: the caller zeroes it, the calls write
+ *               NSA_CODE_CACHE into it when they skipped a token (a page table entry out of
+ *               range, a position outside the sequence's capacity or the rotation's table, a
+ *               length out of range).  nsa_device_status reads it.
+ *
+ * 4 bits: a group x[0..31] of consecutive values of a row is kept as codes c and (s, z):
+ *   lo, hi = min x, max x;  s = bf16((hi - lo) * (1/15)), 0 if that is below 2^-100;
+ *   z = bf16(lo + 8 s);  c = clamp(round((x - z) * (1 / s)) + 8, 0, 15), 8 if s = 0,
+ * each operation in fp32, round to nearest even; a code stands for s (c - 8) + z.  A group with a
+ * NaN, an infinity or a span beyond fp32 has s = z = NaN.  The order of a row's nibbles (low nibble
+ * of a byte first) is the one the tensor cores read: keys, 32-bit words of 8 consecutive values:
+ * word 4 g + i of the row's values (i = 0..3 in group g) is stored as word i (d / 32) + g; values,
+ * 16-bit halves of 4 consecutive values: half 8 g + i (i = 0..7) is stored as half i (d / 32) + g.
+ */
+typedef enum { NSA_CACHE_BF16 = 0, NSA_CACHE_INT4 = 1 } nsa_cache_format;
+
+/* Status word value: a call on a paged cache skipped a token (see nsa_cache.status). */
+#define NSA_CODE_CACHE 201
+
+typedef struct {
+  int32_t format, batch, h_kv, d_k, d_v, page_size, n_pages, max_pages;
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  const int32_t* page_table;
+  int32_t* status;
+} nsa_cache;
+
+/*
+ * nsa_cache_append -- writes the new tokens of every sequence into the cache, the keys rotated by
+ * their positions on the way.
+ *   seqlens      int32 [B] device: tokens of each sequence with the new ones.
+ *   n_new        new tokens of each sequence when cu_seqlens is NULL: row (b, i) of the inputs
+ *                [B, n_new, ...] is the token at position seqlens[b] - n_new + i.  Rows before
+ *                position 0 (a batch padded at the front) are not written.
+ *   cu_seqlens,  int32 [B + 1] device, or NULL: rows cu[b] .. cu[b+1]-1 of the packed inputs
+ *   total_tokens [total_tokens, ...] are the last cu[b+1] - cu[b] tokens of sequence b.  Rows
+ *                that belong to no sequence are not written.  Read on the device only.
+ *   k, v         bf16, heads and dims contiguous, k_stride / v_stride elements from one token to
+ *                the next (multiples of 8, at least h_kv * d), 16-byte aligned bases: slices of one
+ *                projection's output are taken as they are.
+ *   cos_sin      fp32 [n_positions, rot_dim], 16-byte aligned: row p holds the rot_dim / 2 cosines,
+ *                then the sines, of position p's angles; NULL: no rotation.  rot_dim a multiple
+ *                of 16, at most d_k.  The pair of angle j is (j, j + rot_dim / 2), or
+ *                (2 j, 2 j + 1) with interleaved = 1: (a, b) -> (a cos - b sin, b cos + a sin), each
+ *                product and the sum rounded to fp32, then to bf16; dims from rot_dim on stay.
+ *   q, q_out     optional: the new tokens' queries, bf16 h_q heads of d_k like k (q_stride),
+ *                rotated into q_out [B * n_new or total_tokens, h_q, d_k] (contiguous, not
+ *                overlapping q).  Queries of rows that are not written come out as zeros (with
+ *                cu_seqlens: rows of no sequence are left as they were).
+ * One launch.  Two sequences that share a page must not both append to it.
+ */
+typedef struct {
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  const int32_t* seqlens;
+  const int32_t* cu_seqlens;
+  const float* cos_sin;
+  int64_t k_stride, v_stride, q_stride;
+  int32_t n_new, total_tokens, n_positions, rot_dim, interleaved, h_q;
+} nsa_cache_append_args;
+
+NSA_API nsa_status nsa_cache_append(const nsa_cache* cache, const nsa_cache_append_args* args, void* stream);
+
+/*
+ * nsa_cache_read -- the last tokens of every sequence out of the cache, as contiguous bf16 keys and
+ * values (for nsa_compress, a prompt that continues a cached prefix, or a check).  Rows as for
+ * nsa_cache_append: n_new per sequence into k_out [B, n_new, h_kv, d_k], v_out [B, n_new, h_kv, d_v],
+ * or packed by cu_seqlens into [total_tokens, h_kv, d].  4-bit values are s (c - 8) + z rounded once
+ * to bf16.  Rows before position 0 and rows whose page is out of range come out as zeros; rows
+ * that belong to no sequence are left as they were.  Outputs 16-byte aligned.
+ */
+NSA_API nsa_status nsa_cache_read(const nsa_cache* cache, const int32_t* seqlens, const int32_t* cu_seqlens,
+                                  int32_t n_new, int32_t total_tokens, void* k_out, void* v_out, void* stream);
+
+/*
+ * nsa_cache_attention -- attention of the newest tokens of every sequence over its cache.
+ *   q       bf16 [B, n_new, h_q, d_k]: query i of sequence b is at position
+ *           p = seqlens[b] - n_new + i (the new tokens' keys and values are in the cache already);
+ *           n_new 1 .. 16, h_q a multiple of h_kv with h_q / h_kv <= 16.
+ *   out     bf16 [B, n_new, h_q, d_v]
+ *   seqlens int32 [B] device; clamped into [0, max_seqlen] on the device.  max_seqlen (host):
+ *           1 .. max_pages * page_size.
+ * Query head h attends, in KV head h / (h_q / h_kv), to the positions u in
+ * [max(0, p - window + 1), p] (window 0: all u <= p):
+ *   x = softmax_scale * q.k(u)              (0: 1/sqrt(d_k))
+ *   x = softcap * tanh(x / softcap)         if softcap > 0
+ *   x = x + slopes[h] * (u - p)             if slopes (fp32 [h_q] device) is given
+ * and softmax over u, in fp32; a query with p < 0 gives zeros.  4-bit values enter exactly as
+ * s (c - 8) + z.  lse (optional, fp32 [B, n_new, h_q]): the log of the sum of exp(x), -inf where
+ * there is nothing to attend.  Values of tokens that no query of the sequence attends never
+ * matter; a NaN or an infinity in an attended value can reach all n_new queries.
+ * Workspace: nsa_cache_attention_workspace(cache, args) bytes, 256-byte aligned (0: none is
+ * needed); nothing in it has to be set before or kept after the call.  Results do not depend on the
+ * order in which blocks run.
+ */
+typedef struct {
+  const int32_t* seqlens;
+  const float* slopes;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  float softmax_scale, softcap;
+  int32_t n_new, h_q, max_seqlen, window;
+} nsa_cache_attention_args;
+
+NSA_API size_t nsa_cache_attention_workspace(const nsa_cache* cache, const nsa_cache_attention_args* args);
+NSA_API nsa_status nsa_cache_attention(const nsa_cache* cache, const void* q, const nsa_cache_attention_args* args,
+                                       void* out, void* stream);
+
+/*
  * nsa_compress_append -- keeps a compressed cache current while decoding ([NOTES] §5: each
  * block of l tokens, taken every s tokens, is one compressed key/value; with a growing cache a
  * new block is complete every s tokens).
@@ -423,7 +560,8 @@ NSA_API nsa_status nsa_forward_noalloc(const void* q, const void* k, const void*
  * and the kernel stops issuing work and returns instead of hanging.
  * Synchronises `stream` (a cudaStream_t, NULL = the default stream), reads the word and
  * returns NSA_OK if it is 0, NSA_ERR_INVALID_ARG if it is NSA_CODE_CU_SEQLENS (the contents of
- * a variable-length call's cu_seqlens broke their rules), NSA_ERR_TIMEOUT otherwise (code_out,
+ * a variable-length call's cu_seqlens broke their rules) or NSA_CODE_CACHE (`workspace` is a paged
+ * cache's status word, and a call on that cache skipped a token), NSA_ERR_TIMEOUT otherwise (code_out,
  * if not NULL, receives the word: which wait gave up).  NSA_ERR_INVALID_ARG for a null workspace, NSA_ERR_CUDA if the
  * synchronisation or the copy fails.
  */
