@@ -74,6 +74,8 @@ nsa::CacheAttnArgs attention_args(const nsa_cache* c, const nsa_cache_attention_
   r.seqlens = a->seqlens; r.slopes = a->slopes; r.lse = a->lse; r.workspace = a->workspace;
   r.scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.f / std::sqrt((float)c->d_k);
   r.softcap = a->softcap;
+  r.inv_softcap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;
+  r.inv_softcap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;
   r.n_new = a->n_new; r.h_q = a->h_q; r.G = a->h_q / c->h_kv; r.max_seqlen = a->max_seqlen; r.window = a->window;
   return r;
 }

@@ -1,4 +1,4 @@
-// Attention of the newest tokens over a paged cache in bf16 or 4 bits.
+// Attention of the newest tokens over a paged cache in bf16 or 4 bits.  Bound: the cache's bytes.
 //
 // Per KV head the query rows (n_new tokens x G heads) stand as the MMA's N (tiles of 8) and 16
 // cached tokens as its M, so that a group of 8 heads wastes nothing:
@@ -7,14 +7,30 @@
 //   O^T[d, row] += V^T P^T    A = V^T: a register pairs two tokens of one dim (byte permutes), and
 //                             the tile's dims are permuted to match.  S's C fragment becomes
 //                             P^T's B fragment by movmatrix.
-// Keys in 4 bits: (w >> 8 i) & 0x000f000f and & 0x00f000f0 are pairs of f16 subnormals c 2^-24 and
-// c 2^-20, which the tensor cores multiply exactly: no conversion.  The queries of the latter are
-// divided by 16, and every query row is scaled by a power of two so that f16 holds it.  The
-// group's (s, z) come in behind the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q.
-// Values in 4 bits: codes become the bf16 integers c - 8 and P is scaled by the token's s (one
-// rounding); P z is summed in fp32.
-// The keys of a sequence are split over blocks, a block's over its warps; the parts are joined
-// by their maxima and sums in a fixed order.  Bound: the cache's bytes.
+// The operands come from registers (warp-level MMA): in 4 bits a tcgen05 form would have to write
+// every widened value to shared memory and read it back, 640 bytes a token against the 200 that
+// are stored, which alone takes longer than the cache's bytes.
+//
+// Keys in 4 bits: w & 0x0f0f0f0f are four e4m3 values c 2^-9 (subnormals and the first binade are
+// one linear run), which the tensor cores multiply exactly: no conversion.  A query is the sum of
+// two e4m3 values, exactly where it is at least 2^-9 of its row's largest and within 2^-18 of that
+// elsewhere (rows are scaled by powers of two).  The e4m3 MMA (K = 32, one group) takes 4.3 cycles
+// a warp against 8.1 of the 16-bit one with half the K.  A group's (s, z) come in behind
+// the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as one more MMA with
+// the stored pairs as A and the groups' query sums (two bf16 terms, 2^-18) as B.
+//
+// Values in 4 bits: w & 0x000f000f and w & 0x00f000f0 are pairs of f16 subnormals c 2^-24 and
+// c 2^-20, multiplied exactly as well.  A token's weight is P s 2^k in f16 (one rounding, 2^-11),
+// k by group from the largest s met so far, so that weights stay below 2^15; weights below 2^-40 of
+// that limit vanish.  P (z - 8 s) is summed in fp32.  The tensor cores cut off sums instead
+// of rounding them (measured: 4096 steps lose 2e-4), so every 32 tiles the offset's sum is taken into
+// the accumulators, which leaves them at the size of the result.
+//
+// Every warp copies its own tiles of 16 tokens into a ring in shared memory (cp.async, no block-wide
+// waits).  The tiles of all sequences and heads are laid end to end and cut into equal runs, one
+// per block, so unequal lengths and head counts fill the GPU alike; a sequence cut into several runs
+// leaves a part in each block's slots and a second small kernel joins the parts by their maxima and
+// sums, in a fixed order.
 #include <algorithm>
 
 #include "cache.cuh"
@@ -22,14 +38,20 @@
 namespace nsa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kTile = 16;   // tokens per step of a warp
+constexpr int kTile = 16;         // tokens per step of a warp
+constexpr int kFlush = 32;        // tiles between two corrections of the accumulators
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -43,29 +65,62 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// two fp32 values as e4m3 (low byte first), and back
+__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3(uint32_t x) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
 
-// N 32-bit words from global memory, as wide as 8-byte alignment (16 for N = 4) allows
+// copies of 8 or 16 bytes into shared memory; `on` false: zeros
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool on) {
+  const int n = on ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n));
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n));
+}
+// N 32-bit words from shared memory, as wide as 8-byte alignment (16 for multiples of 4) allows
 template <int N>
-__device__ __forceinline__ void ld_words(uint32_t (&w)[N], const void* p) {
-  if constexpr (N == 4) {
-    const uint4 u = __ldg(static_cast<const uint4*>(p));
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+__device__ __forceinline__ void lds_words(uint32_t (&w)[N], const char* p) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p + 16 * i);
+      w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+    }
   } else if constexpr (N % 2 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-      const uint2 u = __ldg(static_cast<const uint2*>(p) + i);
+      const uint2 u = *reinterpret_cast<const uint2*>(p + 8 * i);
       w[2 * i] = u.x; w[2 * i + 1] = u.y;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __ldg(static_cast<const uint32_t*>(p) + i);
+    for (int i = 0; i < N; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 4 * i);
   }
 }
 
 // cap tanh(x / cap): 1 - 2 / (e^2t + 1), and for small t, where that loses the digits of t, the
 // series t - t^3/3 + 2 t^5/15 - 17 t^7/315 + 62 t^9/2835 (the next term is below 1e-8 t at t = 1/4).
-__device__ __forceinline__ float capped(float x, float cap) {
-  const float t = x / cap, t2 = t * t;
+__device__ __forceinline__ float capped(float x, float cap, float inv_cap) {
+  const float t = x * inv_cap, t2 = t * t;
   const float big = 1.f - __fdividef(2.f, ex2(t * (2.f * kLog2e)) + 1.f);
   float p = fmaf(t2, 62.f / 2835.f, -17.f / 315.f);
   p = fmaf(t2, p, 2.f / 15.f);
@@ -77,426 +132,696 @@ __device__ __forceinline__ float capped(float x, float cap) {
 // 2^(-inf - kNone) is 0 (a masked token) and 2^(NaN - kNone) a NaN (an attended one).
 constexpr float kNone = -3.0e38f;
 
-// The keys a tile of rows attends to, of one sequence: [lo, hi), cut into n parts of `chunk` from
-// base on; rows see [p - window + 1, p] with p = p0 + (row's token).
-struct Span {
-  int p0, lo, hi, base, n;
+// How a call is cut.  whole: one block per (sequence, head, tile of rows).  Else `blocks` blocks share
+// the tiles of all of them in equal runs of at least min_tiles.
+struct Plan {
+  int row_tiles, tile_rows;   // row tiles per head and rows of one
+  int blocks, min_tiles, row_groups;
+  bool whole, nt2;
 };
-__device__ __forceinline__ Span span_of(int len, int n_new, int i0, int i1, int window, int chunk) {
+
+// A block that holds the first part of an item cut over blocks says here which blocks hold the rest.
+struct Cut {
+  int b, head_tile, last, rows;   // last < 0: nothing to join
+};
+
+// The keys a tile of rows attends to, of one sequence: [lo, hi), in `tiles` tiles from base on.
+struct Span {
+  int p0, lo, hi, base, tiles;
+};
+__device__ __forceinline__ Span span_of(int len, int n_new, int i0, int i1, int window) {
   Span s;
   s.p0 = len - n_new;
   s.hi = max(0, s.p0 + i1 + 1);
   s.lo = window > 0 ? max(0, s.p0 + i0 - window + 1) : 0;
   s.base = s.lo & ~(kTile - 1);
-  s.n = s.hi > s.base ? (s.hi - s.base + chunk - 1) / chunk : 1;
+  s.tiles = max(1, (s.hi - s.base + kTile - 1) / kTile);
   return s;
 }
-
-__device__ __forceinline__ int seq_len_clamped(const CacheArgs& c, const CacheAttnArgs& a, int b, bool tell) {
-  const int n = __ldg(a.seqlens + b);
-  if (tell && (n < 0 || n > a.max_seqlen)) cache::report(c.status);
-  return min(max(n, 0), a.max_seqlen);
+__device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, int b, int rt) {
+  const int len = min(max(__ldg(a.seqlens + b), 0), a.max_seqlen);
+  const int r0 = rt * p.tile_rows, r1 = min(a.n_new * a.G, r0 + p.tile_rows);
+  return span_of(len, a.n_new, r0 / a.G, (r1 - 1) / a.G, a.window);
 }
 
-template <bool INT4, int DK, int DV, int NT>
-struct Frag {   // registers of one 16-token tile
-  static constexpr int NG = DK / 32, NH = DV / 32;
-  uint32_t k[2][INT4 ? NG : DK / 8];    // rows lane / 4 and lane / 4 + 8
-  uint32_t v[4][INT4 ? NH / 2 : DV / 16];   // tokens 2q, 2q+1, 2q+8, 2q+9 (q = lane % 4)
-  uint32_t ks[2][INT4 ? NG : 1], vs[2][INT4 ? NH : 1];
+// One tile of 16 tokens as a stage of the ring holds it.  4 bits: key codes, value codes, (s, z) pairs of
+// keys and of values; rows of values lie with their 16-byte units turned by the row, so that the
+// lanes' loads spread over the banks.  bf16: key rows, value rows, units turned likewise.
+template <bool INT4, int DK, int DV>
+struct Stage {
+  static constexpr int kRowK = INT4 ? DK / 2 : DK * 2, kRowV = INT4 ? DV / 2 : DV * 2;
+  static constexpr int kRowKs = INT4 ? DK / 8 : 0, kRowVs = INT4 ? DV / 8 : 0;
+  static constexpr int kV = kTile * kRowK, kKs = kV + kTile * kRowV, kVs = kKs + kTile * kRowKs;
+  static constexpr int kBytes = kVs + kTile * kRowVs;
+  __device__ static int key_unit(int row, int u) { return INT4 ? u : u ^ ((row & 1) << 2); }
+  __device__ static int value_unit(int row, int u) {
+    if constexpr (INT4) return DV == 128 ? u ^ ((row >> 1) & 3) : u;
+    return u ^ (((row >> 1) & 3) << 1);
+  }
 };
 
-template <bool INT4, int DK, int DV, int NT, bool EXT>
-__global__ void __launch_bounds__(kWarps * 32)
-cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, int chunk, int splits, int row_tiles,
-                  float* __restrict__ part_o, float2* __restrict__ part_ml) {
+// rows [0, 16) of ROW bytes, `stride` apart in memory, into the stage; FULL: no row is left out
+template <int ROW, bool FULL, class Unit>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const char* src, size_t stride, int lane, int lo, int hi, Unit unit) {
+  constexpr int kBytes = ROW % 16 == 0 ? 16 : 8, kUnits = ROW / kBytes, kAll = kTile * kUnits;
+#pragma unroll
+  for (int i = 0; i < (kAll + 31) / 32; ++i) {
+    const int x = lane + 32 * i;
+    if (kAll % 32 == 0 || x < kAll) {
+      const int row = x / kUnits, u = x % kUnits;
+      copy_async<kBytes>(dst + row * ROW + unit(row, u) * kBytes, src + row * stride + u * kBytes,
+                         FULL || (row >= lo && row < hi));
+    }
+  }
+}
+
+template <bool INT4, int DK, int DV, bool FULL>
+__device__ __forceinline__ void copy_tile(const CacheArgs& c, uint32_t dst, int page, int off, int h, int lane, int lo, int hi) {
+  using T = Stage<INT4, DK, DV>;
+  const auto ku = [](int r, int u) { return T::key_unit(r, u); };
+  const auto vu = [](int r, int u) { return T::value_unit(r, u); };
+  const auto same = [](int, int u) { return u; };
+  const char *k = static_cast<const char*>(c.k), *v = static_cast<const char*>(c.v);
+  if constexpr (INT4) {
+    const size_t row = ((size_t)page * c.h_kv + h) * c.page_size + off;
+    copy_rows<T::kRowK, FULL>(dst, k + row * T::kRowK, T::kRowK, lane, lo, hi, ku);
+    copy_rows<T::kRowV, FULL>(dst + T::kV, v + row * T::kRowV, T::kRowV, lane, lo, hi, vu);
+    copy_rows<T::kRowKs, FULL>(dst + T::kKs, static_cast<const char*>(c.k_scale) + row * T::kRowKs, T::kRowKs, lane, lo, hi, same);
+    copy_rows<T::kRowVs, FULL>(dst + T::kVs, static_cast<const char*>(c.v_scale) + row * T::kRowVs, T::kRowVs, lane, lo, hi, same);
+  } else {
+    const size_t row = ((size_t)page * c.page_size + off) * c.h_kv + h;
+    copy_rows<T::kRowK, FULL>(dst, k + row * T::kRowK, (size_t)c.h_kv * T::kRowK, lane, lo, hi, ku);
+    copy_rows<T::kRowV, FULL>(dst + T::kV, v + row * T::kRowV, (size_t)c.h_kv * T::kRowV, lane, lo, hi, vu);
+  }
+}
+
+template <bool INT4, int DK, int DV, int NT, int W, int S>
+constexpr int attn_smem() {
+  return W * std::max(S * Stage<INT4, DK, DV>::kBytes, NT * 8 * (DV + 4 + 2) * 4);
+}
+
+template <bool INT4, int DK, int DV, int NT, int W, int MINB, int S, bool EXT>
+__global__ void __launch_bounds__(W * 32, MINB)
+cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* __restrict__ cuts, float2* __restrict__ part_ml,
+                  float* __restrict__ part_o) {
+  using T = Stage<INT4, DK, DV>;
   constexpr int NG = DK / 32, NH = DV / 32, MT = DV / 16, KS = DK / 16;
-  extern __shared__ float smem[];
+  constexpr int kCols = NT * 8, kRow = DV + 4;
+  constexpr int kWarpBytes = attn_smem<INT4, DK, DV, NT, W, S>() / W;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ long long s_scan[W];
+  __shared__ long long s_off;
+  __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, q4 = lane & 3;
-  int bid = blockIdx.x;
-  const int rt = bid % row_tiles; bid /= row_tiles;
-  const int h = bid % c.h_kv; bid /= c.h_kv;
-  const int split = bid % splits, b = bid / splits;
-  const int R = a.n_new * a.G, r0 = rt * NT * 8, r1 = min(R, r0 + NT * 8);
-  const int i0 = r0 / a.G, i1 = (r1 - 1) / a.G;
-  const int len = seq_len_clamped(c, a, b, threadIdx.x == 0 && split == 0 && h == 0 && rt == 0);
-  const Span sp = span_of(len, a.n_new, i0, i1, a.window, chunk);
-  if (split >= sp.n) return;
+  const int rg = warp % pl.row_groups, streams = W / pl.row_groups, ts = warp / pl.row_groups;
+  const int R = a.n_new * a.G;
+  char* ring = smem + warp * kWarpBytes;
+  const uint32_t ring_u = smem_u32(ring);
 
-  // ---- queries as B fragments: row n = lane / 4 of each tile of 8
-  uint32_t qf[NT][KS][2];
-  float qz[INT4 ? NT : 1][NG][2];   // 4 bits: the sum of each group's queries, for columns 2q, 2q+1
-  float sc[NT][2];                  // what a column's raw score is multiplied by (natural units)
-  int pos[NT][2];                   // the columns' positions
-  float slope[EXT ? NT : 1][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = min(r0 + nt * 8 + g8, R - 1), i = r / a.G, g = r - i * a.G;
-    const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
-    if constexpr (!INT4) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
-        qf[nt][ks][0] = u.x;
-        qf[nt][ks][1] = u.y;
-      }
-      sc[nt][0] = sc[nt][1] = a.scale;
-    } else {
-      uint4 u[NG];
-      float amax = 0.f;
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
-        const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          amax = fmaxf(amax, fmaxf(fabsf(cache::bf16_lo(w[e])), fabsf(cache::bf16_hi(w[e]))));
-      }
-      amax = warp_max4(amax);
-      // a power of two that takes the row's largest query into [2^13, 2^14)
-      int e2 = (int)((__float_as_uint(amax) >> 23) & 255u);
-      e2 = (e2 == 0 || e2 == 255) ? 0 : 13 - (e2 - 127);
-      e2 = min(max(e2, -120), 120);
-      const float up = __uint_as_float((uint32_t)(e2 + 127) << 23), down = __uint_as_float((uint32_t)(127 - e2) << 23);
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
-        float x[8], sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] = cache::bf16_lo(w[e]) * up;
-          x[2 * e + 1] = cache::bf16_hi(w[e]) * up;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += x[e];
-        const __half2 b00 = __floats2half2_rn(x[0], x[4]), b01 = __floats2half2_rn(x[1] * 0.0625f, x[5] * 0.0625f);
-        const __half2 b10 = __floats2half2_rn(x[2], x[6]), b11 = __floats2half2_rn(x[3] * 0.0625f, x[7] * 0.0625f);
-        qf[nt][2 * gr][0] = *reinterpret_cast<const uint32_t*>(&b00);
-        qf[nt][2 * gr][1] = *reinterpret_cast<const uint32_t*>(&b01);
-        qf[nt][2 * gr + 1][0] = *reinterpret_cast<const uint32_t*>(&b10);
-        qf[nt][2 * gr + 1][1] = *reinterpret_cast<const uint32_t*>(&b11);
-        sum = warp_sum4(sum);
-        // the products carry 2^-24 (the subnormals): so does the sum beside them
-        sum *= 0x1p-24f;
-        qz[nt][gr][0] = __shfl_sync(0xffffffffu, sum, 8 * q4);
-        qz[nt][gr][1] = __shfl_sync(0xffffffffu, sum, 8 * q4 + 4);
-      }
-      const float f = a.scale * down;
-      sc[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
-      sc[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int rc = min(r0 + nt * 8 + 2 * q4 + j, R - 1), ic = rc / a.G;
-      pos[nt][j] = sp.p0 + ic;
-      if constexpr (EXT) slope[nt][j] = a.slopes ? __ldg(a.slopes + h * a.G + rc - ic * a.G) * kLog2e : 0.f;
+  if (c.status) {   // lengths out of range are told of once
+    for (long long b = (long long)blockIdx.x * blockDim.x + threadIdx.x; b < c.batch; b += (long long)gridDim.x * blockDim.x) {
+      const int n = __ldg(a.seqlens + b);
+      if (n < 0 || n > a.max_seqlen) cache::report(c.status);
     }
   }
 
-  float o[MT][NT][4];
-  float m[NT][2], l[NT][2], zacc[INT4 ? NT : 1][NH][2];
+  // ---- which tiles are this block's: `left` of them from tile t of item (b, h, rt) on
+  int b, h, rt, t = 0;
+  long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles
+  if (pl.whole) {
+    int id = blockIdx.x;
+    rt = id % pl.row_tiles; id /= pl.row_tiles;
+    h = id % c.h_kv;
+    b = id / c.h_kv;
+    left = span_of(c, a, pl, b, rt).tiles;
+  } else {
+    const auto weight = [&](int bb) {
+      long long w = 0;
+      for (int x = 0; x < pl.row_tiles; ++x) w += span_of(c, a, pl, bb, x).tiles;
+      return w * c.h_kv;
+    };
+    const int strip = (c.batch + W * 32 - 1) / (W * 32);
+    const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
+    long long mine = 0;
+    for (int x = b0; x < b1; ++x) mine += weight(x);
+    long long upto = mine;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      m[nt][j] = kNone;
-      l[nt][j] = 0.f;
-      if constexpr (INT4) {
-#pragma unroll
-        for (int gr = 0; gr < NH; ++gr) zacc[nt][gr][j] = 0.f;
-      }
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
     }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    long long total = 0;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) upto += s_scan[w];
+      total += s_scan[w];
+    }
+    per = max((long long)pl.min_tiles, (total + gridDim.x - 1) / gridDim.x);
+    pos0 = per * blockIdx.x;
+    if (pos0 >= total) {
+      if (threadIdx.x == 0) cuts[blockIdx.x] = Cut{0, 0, -1, 0};
+      return;
+    }
+    if (upto - mine <= pos0 && pos0 < upto) {
+      long long off = pos0 - (upto - mine);
+      int x = b0;
+      for (long long w; off >= (w = weight(x)); ++x) off -= w;
+      s_b = x;
+      s_off = off;
+    }
+    __syncthreads();
+    b = s_b;
+    const long long head = weight(b) / c.h_kv;
+    h = (int)(s_off / head);
+    t = (int)(s_off % head);
+    rt = 0;
+    for (int n; t >= (n = span_of(c, a, pl, b, rt).tiles); ++rt) t -= n;
+    left = min(per, total - pos0);
   }
 
-  // ---- this warp's run of tiles
-  const int start = sp.base + split * chunk, stop = min(sp.hi, start + chunk);
-  const int tiles = (max(0, stop - start) + kTile - 1) / kTile, per = (tiles + kWarps - 1) / kWarps;
-  const int t1 = min(tiles, (warp + 1) * per);
-  // tiles inside [all_lo, all_hi) are seen whole by every row
-  const int all_lo = a.window > 0 ? sp.p0 + i1 - a.window + 1 : 0, all_hi = sp.p0 + i0 + 1;
-
-  for (int t = warp * per; t < t1; ++t) {
-    const int u0 = start + t * kTile;
-    const int pj = u0 / c.page_size;
-    const int page = __ldg(c.page_table + (size_t)b * c.max_pages + pj);
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0) cache::report(c.status);
-      continue;
+  Cut cut{0, 0, -1, 0};
+  while (left > 0) {
+    const Span sp = span_of(c, a, pl, b, rt);
+    const int take = (int)min(left, (long long)(sp.tiles - t));
+    const int r0 = rt * pl.tile_rows + rg * kCols;   // this warp's first row (maybe behind the last)
+    if (t == 0 && take < sp.tiles) {
+      cut.b = b;
+      cut.head_tile = h * pl.row_tiles + rt;
+      cut.last = (int)((pos0 + sp.tiles - 1) / per);
+      cut.rows = min(R - rt * pl.tile_rows, pl.tile_rows);
     }
-    const int off = u0 - pj * c.page_size;   // place of the tile's first token
-    // places of this lane's tokens; those outside [lo, hi) are masked, and load a row inside
-    const int c_lo = max(0, sp.lo - u0), c_hi = min(kTile, sp.hi - u0) - 1;
-    Frag<INT4, DK, DV, NT> f;
-    const size_t head_row = ((size_t)page * c.h_kv + h) * c.page_size + off;   // 4 bits
-    const size_t tok_row = ((size_t)page * c.page_size + off) * c.h_kv + h;    // bf16
+
+    // ---- queries as B fragments: row n = lane / 4 of each tile of 8
+    uint32_t qf[NT][KS][2];
+    uint32_t qz[INT4 ? NT : 1][2][2];   // 4 bits: (-8 sum, sum) of the queries of groups q4 and q4 + 4, two terms
+    float sc[NT][2];                    // what a column's raw score is multiplied by (natural units)
+    int pos[NT][2];                     // the columns' positions
+    float slope[EXT ? NT : 1][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int x = min(max(g8 + 8 * j, c_lo), c_hi);
-      if constexpr (INT4) {
-        ld_words<NG>(f.k[j], static_cast<const uint8_t*>(c.k) + (head_row + x) * (DK / 2) + q4 * (NG * 4));
-        ld_words<NG>(f.ks[j], static_cast<const uint8_t*>(c.k_scale) + (head_row + x) * (NG * 4));
-        ld_words<NH>(f.vs[j], static_cast<const uint8_t*>(c.v_scale) + (head_row + x) * (NH * 4));
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = min(r0 + nt * 8 + g8, R - 1), i = r / a.G, g = r - i * a.G;
+      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
+      if constexpr (!INT4) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
+          qf[nt][ks][0] = u.x;
+          qf[nt][ks][1] = u.y;
+        }
+        sc[nt][0] = sc[nt][1] = a.scale;
       } else {
-        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + (tok_row + (size_t)x * c.h_kv) * DK);
+        uint4 u[NG];
+        float amax = 0.f, odd = 0.f;   // odd: NaN as soon as one query is not finite
 #pragma unroll
-        for (int i = 0; i < DK / 32; ++i) {
-          const uint4 u = __ldg(row + 4 * i + q4);
-          f.k[j][4 * i] = u.x; f.k[j][4 * i + 1] = u.y; f.k[j][4 * i + 2] = u.z; f.k[j][4 * i + 3] = u.w;
-        }
-      }
-    }
+        for (int gr = 0; gr < NG; ++gr) {
+          u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
+          const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int x = min(max(2 * q4 + (j & 1) + 8 * (j >> 1), c_lo), c_hi);
-      if constexpr (INT4) {
-        ld_words<NH / 2>(f.v[j], static_cast<const uint8_t*>(c.v) + (head_row + x) * (DV / 2) + g8 * (NH * 2));
-      } else {
-        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + (tok_row + (size_t)x * c.h_kv) * DV);
-#pragma unroll
-        for (int i = 0; i < DV / 64; ++i) {
-          const uint4 u = __ldg(row + 8 * i + g8);
-          f.v[j][4 * i] = u.x; f.v[j][4 * i + 1] = u.y; f.v[j][4 * i + 2] = u.z; f.v[j][4 * i + 3] = u.w;
-        }
-      }
-    }
-
-    // ---- S = K Q^T
-    float s[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-    if constexpr (INT4) {
-#pragma unroll
-      for (int gr = 0; gr < NG; ++gr) {
-        const uint32_t w0 = f.k[0][gr], w1 = f.k[1][gr], x0 = w0 >> 8, x1 = w1 >> 8;
-        const float s0 = cache::bf16_lo(f.ks[0][gr]), s1 = cache::bf16_lo(f.ks[1][gr]);
-        const float z0 = fmaf(-8.f, s0, cache::bf16_hi(f.ks[0][gr])), z1 = fmaf(-8.f, s1, cache::bf16_hi(f.ks[1][gr]));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(acc, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][2 * gr][0],
-                  qf[nt][2 * gr][1]);
-          mma_f16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[nt][2 * gr + 1][0],
-                  qf[nt][2 * gr + 1][1]);
-          s[nt][0] += s0 * acc[0] + z0 * qz[nt][gr][0];
-          s[nt][1] += s0 * acc[1] + z0 * qz[nt][gr][1];
-          s[nt][2] += s1 * acc[2] + z1 * qz[nt][gr][0];
-          s[nt][3] += s1 * acc[3] + z1 * qz[nt][gr][1];
-        }
-      }
-    } else {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_bf16(s[nt], f.k[0][2 * ks], f.k[1][2 * ks], f.k[0][2 * ks + 1], f.k[1][2 * ks + 1], qf[nt][ks][0],
-                   qf[nt][ks][1]);
-    }
-
-    // ---- softmax: scores in log2 units, the reference moved only when a score passes it by 8
-    const bool inner = u0 >= all_lo && u0 + kTile <= all_hi;
-    bool move = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = e & 1, u = u0 + g8 + 8 * (e >> 1);
-        float x = s[nt][e] * sc[nt][j];
-        if constexpr (INT4) x *= 0x1p24f;
-        if constexpr (EXT) {
-          if (a.softcap > 0.f) x = capped(x, a.softcap);
-          x = fmaf(x, kLog2e, slope[nt][j] * (float)(u - pos[nt][j]));
-        } else {
-          x *= kLog2e;
-        }
-        if (!inner) {
-          const int p = pos[nt][j];
-          if (u > p || u < sp.lo || (a.window > 0 && u <= p - a.window)) x = -INFINITY;
-        }
-        s[nt][e] = x;
-        move |= x > m[nt][j] + 8.f;
-      }
-    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = fmaxf(s[nt][j], s[nt][j + 2]);
-#pragma unroll
-          for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          x = fmaxf(x, m[nt][j]);
-          const float k = ex2(m[nt][j] - x);
-          m[nt][j] = x;
-          l[nt][j] *= k;
-          if constexpr (INT4) {
-#pragma unroll
-            for (int gr = 0; gr < NH; ++gr) zacc[nt][gr][j] *= k;
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            o[mt][nt][j] *= k;
-            o[mt][nt][j + 2] *= k;
+          for (int e = 0; e < 4; ++e) {
+            amax = fmaxf(amax, fmaxf(fabsf(cache::bf16_lo(w[e])), fabsf(cache::bf16_hi(w[e]))));
+            odd = fmaf(cache::bf16_lo(w[e]), 0.f, fmaf(cache::bf16_hi(w[e]), 0.f, odd));
           }
         }
-    }
+        amax = warp_max4(amax);
+        odd = warp_sum4(odd);
+        // a power of two that takes the row's largest query into [2^7, 2^8)
+        const int e2 = min(max(7 - ((int)((__float_as_uint(amax) >> 23) & 255u) - 127), -120), 120);
+        const float up = pow2(e2);
+        float hi_sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int gr = 0; gr < NG; ++gr) {
+          const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
+          float x[8], sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = ex2(s[nt][e] - m[nt][e & 1]);
-        s[nt][e] = p;
-        l[nt][e & 1] += p;
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = cache::bf16_lo(w[e]) * up;
+            x[2 * e + 1] = cache::bf16_hi(w[e]) * up;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum += x[e];
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {   // even dims, odd dims: the first term and what it leaves
+            const uint32_t t0 = to_e4m3(x[o], x[o + 2]), t1 = to_e4m3(x[o + 4], x[o + 6]);
+            const float2 f0 = from_e4m3(t0), f1 = from_e4m3(t1);
+            qf[nt][2 * gr][o] = t0 | t1 << 16;
+            qf[nt][2 * gr + 1][o] = to_e4m3(x[o] - f0.x, x[o + 2] - f0.y) | to_e4m3(x[o + 4] - f1.x, x[o + 6] - f1.y) << 16;
+          }
+          sum = warp_sum4(sum) * 0x1p-9f;   // the products carry 2^-9: so do the sums beside them
+          if (gr % 4 == q4) hi_sum[gr / 4] = sum;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float top = __bfloat162float(__float2bfloat16_rn(hi_sum[x])), rest = hi_sum[x] - top;
+          qz[nt][0][x] = pack_bf16(-8.f * top, top);
+          qz[nt][1][x] = pack_bf16(-8.f * rest, rest);
+        }
+        const float f = fminf(a.scale * pow2(-e2) * 512.f, 1e38f) + odd;
+        sc[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
+        sc[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int rc = min(r0 + nt * 8 + 2 * q4 + j, R - 1), ic = rc / a.G;
+        pos[nt][j] = sp.p0 + ic;
+        if constexpr (EXT) slope[nt][j] = a.slopes ? __ldg(a.slopes + h * a.G + rc - ic * a.G) * kLog2e : 0.f;
+        else sc[nt][j] *= kLog2e;
+      }
+    }
 
-    // ---- O^T += V^T P^T
+    float o[MT][NT][4];
+    float m[NT][2], l[NT][2], zacc[INT4 ? NT : 1][NH][2];
+    float top_s[INT4 ? NH : 1];   // 2^k of each group's weights
+    uint32_t max_s[INT4 ? NH : 1];   // the largest s that k allows, as bf16 bits
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[nt][j] = kNone;
+        l[nt][j] = 0.f;
+        if constexpr (INT4) {
+#pragma unroll
+          for (int gr = 0; gr < NH; ++gr) zacc[nt][gr][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+    }
     if constexpr (INT4) {
 #pragma unroll
       for (int gr = 0; gr < NH; ++gr) {
-        uint32_t pb[NT][2];
-        const float s0 = cache::bf16_lo(f.vs[0][gr]), s1 = cache::bf16_lo(f.vs[1][gr]);
-        const float z0 = cache::bf16_hi(f.vs[0][gr]), z1 = cache::bf16_hi(f.vs[1][gr]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = movmatrix(pack_bf16(s[nt][0] * s0, s[nt][1] * s0));
-          pb[nt][1] = movmatrix(pack_bf16(s[nt][2] * s1, s[nt][3] * s1));
-          zacc[nt][gr][0] += s[nt][0] * z0 + s[nt][2] * z1;
-          zacc[nt][gr][1] += s[nt][1] * z0 + s[nt][3] * z1;
-        }
-        const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
-        const uint32_t lo = __byte_perm(f.v[0][gr / 2], f.v[1][gr / 2], sel);
-        const uint32_t hi = __byte_perm(f.v[2][gr / 2], f.v[3][gr / 2], sel);
-        uint32_t al[4], ah[4];
-        const uint32_t magic = 0x43004300u, off8 = 0x43084308u;   // 128 + c and 136 in bf16
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint32_t x = ((lo >> (4 * n)) & 0x000f000fu) | magic, y = ((hi >> (4 * n)) & 0x000f000fu) | magic;
-          const __nv_bfloat162 e = *reinterpret_cast<const __nv_bfloat162*>(&off8);
-          const __nv_bfloat162 dx = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), e);
-          const __nv_bfloat162 dy = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), e);
-          al[n] = *reinterpret_cast<const uint32_t*>(&dx);
-          ah[n] = *reinterpret_cast<const uint32_t*>(&dy);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_bf16(o[2 * gr][nt], al[0], al[1], ah[0], ah[1], pb[nt][0], pb[nt][1]);
-          mma_bf16(o[2 * gr + 1][nt], al[2], al[3], ah[2], ah[3], pb[nt][0], pb[nt][1]);
-        }
-      }
-    } else {
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        pb[nt][0] = movmatrix(pack_bf16(s[nt][0], s[nt][1]));
-        pb[nt][1] = movmatrix(pack_bf16(s[nt][2], s[nt][3]));
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {   // word mt holds dims 2 mt and 2 mt + 1 of the lane's eight
-        const uint32_t a0 = __byte_perm(f.v[0][mt], f.v[1][mt], 0x5410), a1 = __byte_perm(f.v[0][mt], f.v[1][mt], 0x7632);
-        const uint32_t a2 = __byte_perm(f.v[2][mt], f.v[3][mt], 0x5410), a3 = __byte_perm(f.v[2][mt], f.v[3][mt], 0x7632);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_bf16(o[mt][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+        top_s[gr] = 0x1p100f;
+        max_s[gr] = 0;
       }
     }
-  }
 
-  // ---- join the warps: sums over the lanes of a column, then over the warps through shared memory
-  constexpr int kCols = NT * 8, kRow = DV + 4;
-  float* s_o = smem;                                  // [kWarps][kCols][kRow]
-  float* s_m = smem + kWarps * kCols * kRow;          // [kWarps][kCols]
-  float* s_l = s_m + kWarps * kCols;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int col = nt * 8 + 2 * q4 + j;
-#pragma unroll
-      for (int d = 4; d <= 16; d <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], d);
-      if (g8 == 0) {
-        s_m[warp * kCols + col] = m[nt][j];
-        s_l[warp * kCols + col] = l[nt][j];
+    // ---- this warp's run of tiles, [ta, tb) of the item
+    const int each = (take + streams - 1) / streams;
+    const int ta = t + min(take, ts * each), tb = t + min(take, (ts + 1) * each);
+    // tiles inside [all_lo, all_hi) are seen whole by every row of the block
+    const int row_lo = rt * pl.tile_rows / a.G, row_hi = (min(R, (rt + 1) * pl.tile_rows) - 1) / a.G;
+    const int all_lo = a.window > 0 ? max(0, sp.p0 + row_hi - a.window + 1) : 0, all_hi = sp.p0 + row_lo + 1;
+
+    // the place of the next tile to copy; its page is fetched one tile ahead
+    int cp_t = ta, cp_j = 0, cp_off = 0, cp_page = -1;
+    uint32_t missing = 0;   // stages whose tile has no valid page
+    const int32_t* pages = c.page_table + (size_t)b * c.max_pages;
+    if (ta < tb) {
+      const int u = sp.base + ta * kTile;
+      cp_j = u / c.page_size;
+      cp_off = u - cp_j * c.page_size;
+      if (sp.hi > 0) cp_page = __ldg(pages + cp_j);
+    }
+    const auto copy_next = [&](int stage) {
+      if (cp_t < tb) {
+        const int u0 = sp.base + cp_t * kTile, lo = sp.lo - u0, hi = sp.hi - u0;
+        const uint32_t dst = ring_u + stage * T::kBytes;
+        if (cp_page >= 0 && cp_page < c.n_pages) {
+          missing &= ~(1u << stage);
+          if (lo <= 0 && hi >= kTile) copy_tile<INT4, DK, DV, true>(c, dst, cp_page, cp_off, h, lane, 0, kTile);
+          else copy_tile<INT4, DK, DV, false>(c, dst, cp_page, cp_off, h, lane, lo, hi);
+        } else {
+          missing |= 1u << stage;
+          if (lane == 0 && hi > 0) cache::report(c.status);
+        }
+        ++cp_t;
+        cp_off += kTile;
+        if (cp_off >= c.page_size) {
+          cp_off = 0;
+          ++cp_j;
+          if (cp_t < tb) cp_page = __ldg(pages + cp_j);
+        }
       }
-      float* row = s_o + (warp * kCols + col) * kRow;
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) copy_next(s);
+
+    int stage = 0, since = 0;
+    for (int tile = ta; tile < tb; ++tile) {
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      const bool gone = missing >> stage & 1;
+      copy_next(stage == 0 ? S - 1 : stage - 1);
+      const char* st = ring + stage * T::kBytes;
+      stage = stage == S - 1 ? 0 : stage + 1;
+      if (gone) continue;
+      const int u0 = sp.base + tile * kTile;
+
+      // ---- S = K Q^T
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
       if constexpr (INT4) {
+        uint32_t kw[2][NG], ks[2][NG], kz[4];
 #pragma unroll
-        for (int gr = 0; gr < NH; ++gr) {
-          float z = zacc[nt][gr][j];
+        for (int j = 0; j < 2; ++j) {
+          lds_words<NG>(kw[j], st + (g8 + 8 * j) * T::kRowK + q4 * (NG * 4));
+          lds_words<NG>(ks[j], st + T::kKs + (g8 + 8 * j) * T::kRowKs);
+          const char* row = st + T::kKs + (g8 + 8 * j) * T::kRowKs + q4 * 4;
+          kz[j] = NG >= 4 || q4 < NG ? *reinterpret_cast<const uint32_t*>(row) : 0u;
+          kz[j + 2] = q4 + 4 < NG ? *reinterpret_cast<const uint32_t*>(row + 16) : 0u;
+        }
 #pragma unroll
-          for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-          *reinterpret_cast<float4*>(row + 32 * gr + 4 * g8) =
-              make_float4(o[2 * gr][nt][j] + z, o[2 * gr][nt][j + 2] + z, o[2 * gr + 1][nt][j] + z, o[2 * gr + 1][nt][j + 2] + z);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_bf16(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][0][0], qz[nt][0][1]);
+          mma_bf16(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][1][0], qz[nt][1][1]);
+        }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          const uint32_t w0 = kw[0][gr], w1 = kw[1][gr];
+          const uint32_t e0 = w0 & 0x0f0f0f0fu, e1 = w1 & 0x0f0f0f0fu, o0 = w0 >> 4 & 0x0f0f0f0fu, o1 = w1 >> 4 & 0x0f0f0f0fu;
+          const float s0 = cache::bf16_lo(ks[0][gr]), s1 = cache::bf16_lo(ks[1][gr]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_e4m3(acc, e0, e1, o0, o1, qf[nt][2 * gr][0], qf[nt][2 * gr][1]);
+            mma_e4m3(acc, e0, e1, o0, o1, qf[nt][2 * gr + 1][0], qf[nt][2 * gr + 1][1]);
+            s[nt][0] = fmaf(s0, acc[0], s[nt][0]);
+            s[nt][1] = fmaf(s0, acc[1], s[nt][1]);
+            s[nt][2] = fmaf(s1, acc[2], s[nt][2]);
+            s[nt][3] = fmaf(s1, acc[3], s[nt][3]);
+          }
         }
       } else {
 #pragma unroll
-        for (int mt = 0; mt < MT; mt += 2)
-          *reinterpret_cast<float4*>(row + 64 * (mt / 4) + 8 * g8 + 2 * (mt % 4)) =
-              make_float4(o[mt][nt][j], o[mt][nt][j + 2], o[mt + 1][nt][j], o[mt + 1][nt][j + 2]);
+        for (int i = 0; i < DK / 32; ++i) {
+          const int x = T::key_unit(g8, 4 * i + q4) * 16;   // rows g8 and g8 + 8 turn alike
+          const uint4 k0 = *reinterpret_cast<const uint4*>(st + g8 * T::kRowK + x);
+          const uint4 k1 = *reinterpret_cast<const uint4*>(st + (g8 + 8) * T::kRowK + x);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(s[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+            mma_bf16(s[nt], k0.z, k1.z, k0.w, k1.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+          }
+        }
+      }
+
+      // ---- softmax: scores in log2 units, the reference moved only when a score passes it by 8
+      uint32_t vs[2][INT4 ? NH : 1];
+      bool move = false;
+      if constexpr (INT4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) lds_words<NH>(vs[j], st + T::kVs + (g8 + 8 * j) * T::kRowVs);
+#pragma unroll
+        for (int gr = 0; gr < NH; ++gr) move |= (max_u16x2(vs[0][gr], vs[1][gr]) & 0xffffu) > max_s[gr];
+      }
+      const bool inner = u0 >= all_lo && u0 + kTile <= all_hi;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[nt][e] * sc[nt][e & 1];
+          if constexpr (EXT) {
+            if (a.softcap > 0.f) x = capped(x, a.softcap, a.inv_softcap);
+            x = fmaf(x, kLog2e, slope[nt][e & 1] * (float)(u0 + g8 + 8 * (e >> 1) - pos[nt][e & 1]));
+          }
+          s[nt][e] = x;
+        }
+      if (!inner) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int u = u0 + g8 + 8 * (e >> 1), p = pos[nt][e & 1];
+            if (u > p || u < sp.lo || (a.window > 0 && u <= p - a.window)) s[nt][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) move |= fmaxf(s[nt][j], s[nt][j + 2]) > m[nt][j] + 8.f;
+      if (__any_sync(0xffffffffu, move)) {
+        float grow[INT4 ? NH : 1];
+        if constexpr (INT4) {
+#pragma unroll
+          for (int gr = 0; gr < NH; ++gr) {
+            uint32_t x = max_s[gr];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t y = vs[j][gr] & 0xffffu;
+              if (y < 0x7f80u) x = max(x, y);   // a NaN shows in its products
+            }
+            x = __reduce_max_sync(0xffffffffu, x);
+            x = x ? x | 0x7fu : 0u;             // all of the binade
+            // s 2^k < 2^7: k = 6 - (exponent of s)
+            const int k = x ? min(6 - ((int)(x >> 7) - 127), 100) : 100;
+            const float to = pow2(k);
+            grow[gr] = to / top_s[gr];
+            top_s[gr] = to;
+            max_s[gr] = x;
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float x = fmaxf(s[nt][j], s[nt][j + 2]);
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            x = fmaxf(x, m[nt][j]);
+            const float k = ex2(m[nt][j] - x);
+            m[nt][j] = x;
+            l[nt][j] *= k;
+            if constexpr (INT4) {
+#pragma unroll
+              for (int gr = 0; gr < NH; ++gr) zacc[nt][gr][j] *= k;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const float f = INT4 ? k * grow[INT4 ? mt / 2 : 0] : k;
+              o[mt][nt][j] *= f;
+              o[mt][nt][j + 2] *= f;
+            }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = ex2(s[nt][e] - m[nt][e & 1]);
+          s[nt][e] = p;
+          l[nt][e & 1] += p;
+        }
+
+      // ---- O^T += V^T P^T
+      if constexpr (INT4) {
+        uint32_t vw[4][NH / 2];   // tokens 2q, 2q+1, 2q+8, 2q+9
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = 2 * q4 + (j & 1) + 8 * (j >> 1);
+          const int at = g8 * (NH * 2);
+          lds_words<NH / 2>(vw[j], st + T::kV + row * T::kRowV + T::value_unit(row, at / 16) * 16 + at % 16);
+        }
+#pragma unroll
+        for (int gr = 0; gr < NH; ++gr) {
+          uint32_t pb[NT][2];
+          const float r0s = cache::bf16_lo(vs[0][gr]), r1s = cache::bf16_lo(vs[1][gr]);
+          const float s0 = r0s * top_s[gr], s1 = r1s * top_s[gr];
+          const float z0 = fmaf(-8.f, r0s, cache::bf16_hi(vs[0][gr])), z1 = fmaf(-8.f, r1s, cache::bf16_hi(vs[1][gr]));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            pb[nt][0] = movmatrix(pack_f16(s[nt][0] * s0, s[nt][1] * s0));
+            pb[nt][1] = movmatrix(pack_f16(s[nt][2] * s1, s[nt][3] * s1));
+            zacc[nt][gr][0] = fmaf(s[nt][0], z0, fmaf(s[nt][2], z1, zacc[nt][gr][0]));
+            zacc[nt][gr][1] = fmaf(s[nt][1], z0, fmaf(s[nt][3], z1, zacc[nt][gr][1]));
+          }
+          const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
+          const uint32_t lo = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel), lo8 = lo >> 8;
+          const uint32_t hi = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel), hi8 = hi >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16(o[2 * gr][nt], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, pb[nt][0], pb[nt][1]);
+            mma_f16(o[2 * gr + 1][nt], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, pb[nt][0],
+                    pb[nt][1]);
+          }
+        }
+        if (++since == kFlush) {   // take the offset's sum into the accumulators
+          since = 0;
+#pragma unroll
+          for (int gr = 0; gr < NH; ++gr)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float z = zacc[nt][gr][j];
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+                const float y = z * top_s[gr] * 0x1p-24f;
+                if (fabsf(y) < 0x1p100f) {   // the eight lanes of a column agree
+                  zacc[nt][gr][j] = 0.f;
+                  o[2 * gr][nt][j] += y;
+                  o[2 * gr][nt][j + 2] += 16.f * y;
+                  o[2 * gr + 1][nt][j] += y;
+                  o[2 * gr + 1][nt][j + 2] += 16.f * y;
+                }
+              }
+        }
+      } else {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          pb[nt][0] = movmatrix(pack_bf16(s[nt][0], s[nt][1]));
+          pb[nt][1] = movmatrix(pack_bf16(s[nt][2], s[nt][3]));
+        }
+        const char* vrow = st + T::kV + 2 * q4 * T::kRowV;
+#pragma unroll
+        for (int i = 0; i < DV / 64; ++i) {
+          const int x = T::value_unit(2 * q4, 8 * i + g8) * 16;   // the lane's four rows turn alike
+          const uint4 v0 = *reinterpret_cast<const uint4*>(vrow + x), v1 = *reinterpret_cast<const uint4*>(vrow + T::kRowV + x);
+          const uint4 v2 = *reinterpret_cast<const uint4*>(vrow + 8 * T::kRowV + x);
+          const uint4 v3 = *reinterpret_cast<const uint4*>(vrow + 9 * T::kRowV + x);
+          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+          const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)   // word e holds dims 2 e and 2 e + 1 of the lane's eight
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(o[4 * i + e][nt], __byte_perm(w0[e], w1[e], 0x5410), __byte_perm(w0[e], w1[e], 0x7632),
+                       __byte_perm(w2[e], w3[e], 0x5410), __byte_perm(w2[e], w3[e], 0x7632), pb[nt][0], pb[nt][1]);
+        }
       }
     }
-  __syncthreads();
-  for (int x = threadIdx.x; x < (r1 - r0) * (DV / 4); x += kWarps * 32) {
-    const int col = x / (DV / 4), d = (x % (DV / 4)) * 4, r = r0 + col;
-    float mm = kNone;
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // ---- join the warps of a row group, in the ring's place: sums over the lanes of a column, then over
+    // the warps
+    float* s_o = reinterpret_cast<float*>(ring);   // [kCols][kRow], then maxima and sums
+    float* s_m = s_o + kCols * kRow;
+    float* s_l = s_m + kCols;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * kCols + col]);
-    float ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float k = ex2(s_m[w * kCols + col] - mm);
-      const float4 y = *reinterpret_cast<const float4*>(s_o + (w * kCols + col) * kRow + d);
-      ll += k * s_l[w * kCols + col];
-      acc.x += k * y.x; acc.y += k * y.y; acc.z += k * y.z; acc.w += k * y.w;
+      for (int j = 0; j < 2; ++j) {
+        const int col = nt * 8 + 2 * q4 + j;
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], d);
+        if (g8 == 0) {
+          s_m[col] = m[nt][j];
+          s_l[col] = l[nt][j];
+        }
+        float* row = s_o + col * kRow;
+        if constexpr (INT4) {
+#pragma unroll
+          for (int gr = 0; gr < NH; ++gr) {
+            float z = zacc[nt][gr][j];
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+            const float down = 1.f / top_s[gr];   // powers of two
+            *reinterpret_cast<float4*>(row + 32 * gr + 4 * g8) =
+                make_float4(fmaf(o[2 * gr][nt][j] * 0x1p24f, down, z), fmaf(o[2 * gr][nt][j + 2] * 0x1p20f, down, z),
+                            fmaf(o[2 * gr + 1][nt][j] * 0x1p24f, down, z), fmaf(o[2 * gr + 1][nt][j + 2] * 0x1p20f, down, z));
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < MT; mt += 2)
+            *reinterpret_cast<float4*>(row + 64 * (mt / 4) + 8 * g8 + 2 * (mt % 4)) =
+                make_float4(o[mt][nt][j], o[mt][nt][j + 2], o[mt + 1][nt][j], o[mt + 1][nt][j + 2]);
+        }
+      }
+    __syncthreads();
+    const bool alone = take == sp.tiles;   // else: to the slot of a run that begins (1) or continues (0) the item
+    const size_t slot = (size_t)blockIdx.x * 2 + (t == 0);
+    const int tile_rows = min(R - rt * pl.tile_rows, pl.tile_rows);
+    for (int x = threadIdx.x; x < tile_rows * (DV / 4); x += W * 32) {
+      const int rr = x / (DV / 4), d = (x % (DV / 4)) * 4, col = rr % kCols, r = rt * pl.tile_rows + rr;
+      const char* base = smem + (rr / kCols) * kWarpBytes;   // the first warp of the row's group
+      const size_t step = (size_t)pl.row_groups * kWarpBytes;
+      float mm = kNone;
+      for (int w = 0; w < streams; ++w) mm = fmaxf(mm, reinterpret_cast<const float*>(base + w * step)[kCols * kRow + col]);
+      float ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < streams; ++w) {
+        const float* f = reinterpret_cast<const float*>(base + w * step);
+        const float k = ex2(f[kCols * kRow + col] - mm);
+        const float4 y = *reinterpret_cast<const float4*>(f + col * kRow + d);
+        ll += k * f[kCols * kRow + kCols + col];
+        acc.x += k * y.x; acc.y += k * y.y; acc.z += k * y.z; acc.w += k * y.w;
+      }
+      if (alone) {
+        const int i = r / a.G;
+        const size_t row = ((size_t)b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
+        const float inv = ll > 0.f ? 1.f / ll : ll;   // a NaN stays one; nothing attended: zeros
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + d) =
+            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        if (a.lse && d == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+      } else {
+        const size_t row = slot * pl.tile_rows + rr;
+        *reinterpret_cast<float4*>(part_o + row * DV + d) = acc;
+        if (d == 0) part_ml[row] = make_float2(mm, ll);
+      }
     }
-    if (sp.n == 1) {
-      const int i = r / a.G;
-      const size_t row = ((size_t)b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
-      const float inv = ll > 0.f ? 1.f / ll : ll;   // a NaN stays one; nothing attended: zeros
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + d) =
-          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-      if (a.lse && d == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-    } else {
-      const size_t row = (((size_t)b * c.h_kv + h) * R + r) * splits + split;
-      *reinterpret_cast<float4*>(part_o + row * DV + d) = acc;
-      if (d == 0) part_ml[row] = make_float2(mm, ll);
+    left -= take;
+    pos0 += take;
+    t = 0;
+    if (++rt == pl.row_tiles) {
+      rt = 0;
+      if (++h == c.h_kv) {
+        h = 0;
+        ++b;
+      }
     }
+    if (left > 0) __syncthreads();   // the next item's copies reuse the ring
   }
+  if (!pl.whole && threadIdx.x == 0) cuts[blockIdx.x] = cut;
 }
 
-// Joins the parts of a row: one warp per row, in the order of the parts.
-template <int DV>
-__global__ void cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, int chunk, int splits, int tile_rows,
-                                  const float* __restrict__ part_o, const float2* __restrict__ part_ml) {
+// Joins the parts of the items that were cut: block (x, y) those of the item whose first part block x
+// has, WPR warps per row, the row's parts shared out to them and their sums joined in order.
+constexpr int kJoinWarps = 8;
+template <int DV, int WPR>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const Cut* __restrict__ cuts,
+                  const float2* __restrict__ part_ml, const float* __restrict__ part_o) {
   constexpr int kPer = DV / 32;
-  const int lane = threadIdx.x & 31, R = a.n_new * a.G;
-  const long long id = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (id >= (long long)c.batch * c.h_kv * R) return;
-  const int r = (int)(id % R), h = (int)(id / R % c.h_kv), b = (int)(id / R / c.h_kv);
-  const int r0 = r / tile_rows * tile_rows, r1 = min(R, r0 + tile_rows);
-  const Span sp = span_of(seq_len_clamped(c, a, b, false), a.n_new, r0 / a.G, (r1 - 1) / a.G, a.window, chunk);
-  if (sp.n == 1) return;   // written by the block itself
-  const size_t base = (size_t)id * splits;
+  __shared__ float s_acc[WPR > 1 ? kJoinWarps : 1][DV];
+  __shared__ float2 s_ml[WPR > 1 ? kJoinWarps : 1];
+  const Cut cut = cuts[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+  const int rr = blockIdx.y * (kJoinWarps / WPR) + warp / WPR;
+  if (cut.last < 0 || rr >= cut.rows) return;   // WPR > 1: the whole block
+  const int n = cut.last - (int)blockIdx.x + 1;   // parts: slot 1 of this block, slot 0 of the next ones
+  const auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0)) * pl.tile_rows + rr; };
   float mm = kNone;
-  for (int s = lane; s < sp.n; s += 32) mm = fmaxf(mm, part_ml[base + s].x);
+  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, part_ml[at(i)].x);
 #pragma unroll
   for (int d = 1; d <= 16; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
   float ll = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int s = 0; s < sp.n; ++s) {
-    const float2 ml = part_ml[base + s];
+#pragma unroll 4
+  for (int i = sub; i < n; i += WPR) {
+    const float2 ml = part_ml[at(i)];
     const float k = ex2(ml.x - mm);
     ll += k * ml.y;
-    const float* y = part_o + (base + s) * DV + lane * kPer;
+    const float* y = part_o + at(i) * DV + lane * kPer;
+    float v[kPer];
+    if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += k * y[e];
+    for (int e = 0; e < kPer; ++e) acc[e] += k * v[e];
   }
-  const int i = r / a.G;
-  const size_t row = ((size_t)b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_acc[warp][lane * kPer + e] = acc[e];
+    if (lane == 0) s_ml[warp] = make_float2(0.f, ll);
+    __syncthreads();
+    if (sub) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      ll += s_ml[warp + w].y;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += s_acc[warp + w][lane * kPer + e];
+    }
+  }
+  const int h = cut.head_tile / pl.row_tiles, r = cut.head_tile % pl.row_tiles * pl.tile_rows + rr, i = r / a.G;
+  const size_t row = ((size_t)cut.b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
   const float inv = ll > 0.f ? 1.f / ll : ll;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + lane * kPer);
 #pragma unroll
@@ -504,74 +829,98 @@ __global__ void cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, int 
   if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
-// How a call is cut: rows per block, tokens per block, parts per sequence.
-struct Plan {
-  int nt, row_tiles, chunk, splits;
-  size_t rows;   // parts of rows kept in the workspace
+// Warps per block, blocks per SM and stages of the ring.  Sixteen rows need about 170 registers a
+// thread, eight about 128.
+template <bool INT4, int NT>
+struct Shape {
+  static constexpr int W = INT4 ? (NT == 2 ? 8 : 4) : 8;
+  static constexpr int B = INT4 ? (NT == 2 ? 1 : 3) : 1;
+  static constexpr int S = INT4 ? (NT == 2 ? 6 : 4) : 2;
 };
+int warps_of(bool int4, bool nt2) { return int4 ? (nt2 ? Shape<true, 2>::W : Shape<true, 1>::W) : Shape<false, 1>::W; }
+int blocks_of(bool int4, bool nt2) { return int4 ? (nt2 ? Shape<true, 2>::B : Shape<true, 1>::B) : Shape<false, 1>::B; }
+
+constexpr int kSms = 148;
+constexpr int kWholeTiles = 32;   // items of at most 512 tokens are not cut
 
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   Plan p;
   const int R = a.n_new * a.G;
-  p.nt = R <= 8 ? 1 : 2;
-  p.row_tiles = (R + p.nt * 8 - 1) / (p.nt * 8);
-  // the longest range of keys a block's rows can have, from its first tile on
+  p.nt2 = R > 8;
+  const int W = warps_of(c.int4, p.nt2);
+  p.row_groups = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  p.tile_rows = (p.nt2 ? 16 : 8) * p.row_groups;
+  p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
+  // the most tiles an item can have
   long long range = a.max_seqlen;
   if (a.window > 0) range = std::min<long long>(range, (long long)a.window + a.n_new + kTile);
-  const long long items = (long long)c.batch * c.h_kv * p.row_tiles;
-  const long long slots = 148 * 2;
-  const long long want = std::max<long long>(1, (2 * slots + items - 1) / items);
-  long long chunk = (range + want - 1) / want;
-  chunk = std::max<long long>(kWarps * kTile, (chunk + kWarps * kTile - 1) / (kWarps * kTile) * (kWarps * kTile));
-  p.chunk = (int)chunk;
-  p.splits = (int)((range + chunk - 1) / chunk);
-  p.rows = p.splits > 1 ? (size_t)c.batch * c.h_kv * R * p.splits : 0;
+  const long long tiles = (range + kTile - 1) / kTile, items = (long long)c.batch * c.h_kv * p.row_tiles;
+  p.min_tiles = 2 * (W / p.row_groups);
+  p.whole = tiles <= kWholeTiles;
+  const long long most = (long long)kSms * blocks_of(c.int4, p.nt2);
+  // items <= 2^31 (cache_attn_fits), tiles <= 2^26
+  p.blocks = (int)(p.whole ? std::min<long long>(items, INT32_MAX) : std::min(most, (items * tiles + p.min_tiles - 1) / p.min_tiles));
   return p;
 }
 
+struct Parts {
+  size_t cuts, ml, o, bytes;
+};
+Parts parts_of(const CacheArgs& c, const Plan& p) {
+  Parts x{};
+  if (p.whole) return x;
+  const size_t rows = (size_t)p.blocks * 2 * p.tile_rows;
+  x.ml = (size_t)p.blocks * sizeof(Cut);                    // multiples of 16 bytes throughout
+  x.o = x.ml + rows * sizeof(float2);
+  x.bytes = x.o + rows * c.dv * sizeof(float);
+  return x;
+}
+
 template <bool INT4, int DK, int DV, int NT, bool EXT>
-cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, float* po, float2* pml, cudaStream_t st) {
-  constexpr int kSmem = kWarps * NT * 8 * (DV + 4 + 2) * 4;
+cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, cudaStream_t st) {
+  using H = Shape<INT4, NT>;
+  constexpr int kSmem = attn_smem<INT4, DK, DV, NT, H::W, H::S>();
+  static_assert(kSmem * H::B <= 227 * 1024, "the rings of the resident blocks fit an SM");
   static PerDevice set;
-  auto* f = cache_attn_kernel<INT4, DK, DV, NT, EXT>;
+  auto* f = cache_attn_kernel<INT4, DK, DV, NT, H::W, H::B, H::S, EXT>;
   cudaError_t e = set.once([&] { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)c.batch * p.splits * c.h_kv * p.row_tiles;   // cache_attn_fits
-  f<<<grid, kWarps * 32, kSmem, st>>>(c, a, p.chunk, p.splits, p.row_tiles, po, pml);
+  const Parts x = parts_of(c, p);
+  char* ws = static_cast<char*>(a.workspace);
+  Cut* cuts = reinterpret_cast<Cut*>(ws);
+  float2* ml = reinterpret_cast<float2*>(ws + x.ml);
+  float* o = reinterpret_cast<float*>(ws + x.o);
+  f<<<p.blocks, H::W * 32, kSmem, st>>>(c, a, p, cuts, ml, o);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.whole) return e;
+  // few items, many parts each: a block per row; else a warp per row
+  const long long items = (long long)c.batch * c.h_kv * p.row_tiles;
+  if (items * 16 <= p.blocks)
+    cache_join_kernel<DV, kJoinWarps><<<dim3(p.blocks, p.tile_rows), kJoinWarps * 32, 0, st>>>(c, a, p, cuts, ml, o);
+  else
+    cache_join_kernel<DV, 1><<<dim3(p.blocks, (p.tile_rows + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, st>>>(c, a, p, cuts, ml, o);
   return cudaGetLastError();
 }
 
 template <int DK, int DV>
 cudaError_t launch_dims(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t st) {
   const Plan p = plan_of(c, a);
-  float2* pml = static_cast<float2*>(a.workspace);
-  float* po = reinterpret_cast<float*>(pml + (p.rows + 1) / 2 * 2);
   const bool ext = a.softcap > 0.f || a.slopes;
-  cudaError_t e;
-#define NSA_VARIANT(I, N, X) launch_variant<I, DK, DV, N, X>(c, a, p, po, pml, st)
+#define NSA_VARIANT(I, N, X) launch_variant<I, DK, DV, N, X>(c, a, p, st)
   if (c.int4)
-    e = p.nt == 1 ? (ext ? NSA_VARIANT(true, 1, true) : NSA_VARIANT(true, 1, false))
-                  : (ext ? NSA_VARIANT(true, 2, true) : NSA_VARIANT(true, 2, false));
-  else
-    e = p.nt == 1 ? (ext ? NSA_VARIANT(false, 1, true) : NSA_VARIANT(false, 1, false))
-                  : (ext ? NSA_VARIANT(false, 2, true) : NSA_VARIANT(false, 2, false));
+    return p.nt2 ? (ext ? NSA_VARIANT(true, 2, true) : NSA_VARIANT(true, 2, false))
+                 : (ext ? NSA_VARIANT(true, 1, true) : NSA_VARIANT(true, 1, false));
+  return p.nt2 ? (ext ? NSA_VARIANT(false, 2, true) : NSA_VARIANT(false, 2, false))
+               : (ext ? NSA_VARIANT(false, 1, true) : NSA_VARIANT(false, 1, false));
 #undef NSA_VARIANT
-  if (e != cudaSuccess || p.splits == 1) return e;
-  const long long rows = (long long)c.batch * c.h_kv * a.n_new * a.G;
-  cache_join_kernel<DV><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(c, a, p.chunk, p.splits, p.nt * 8, po, pml);
-  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t cache_attn_workspace(const CacheArgs& c, const CacheAttnArgs& a) {
-  const Plan p = plan_of(c, a);
-  return p.rows ? ((p.rows + 1) / 2 * 2) * sizeof(float2) + p.rows * c.dv * sizeof(float) : 0;
-}
+size_t cache_attn_workspace(const CacheArgs& c, const CacheAttnArgs& a) { return parts_of(c, plan_of(c, a)).bytes; }
 
 bool cache_attn_fits(const CacheArgs& c, const CacheAttnArgs& a) {
-  const Plan p = plan_of(c, a);
-  return (long long)c.batch * c.h_kv * std::max(p.splits * p.row_tiles, a.n_new * a.G) <= INT32_MAX;
+  return (long long)c.batch * c.h_kv * plan_of(c, a).row_tiles <= INT32_MAX;
 }
 
 cudaError_t launch_cache_attn(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t st) {

@@ -240,7 +240,7 @@ struct CacheAttnArgs {
   const int32_t* seqlens;
   const float* slopes;          // optional [h_q]
   void* workspace;
-  float scale, softcap;
+  float scale, softcap, inv_softcap;
   int n_new, h_q, G, max_seqlen, window;
 };
 size_t cache_attn_workspace(const CacheArgs& c, const CacheAttnArgs& a);
