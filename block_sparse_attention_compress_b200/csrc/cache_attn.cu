@@ -11,16 +11,15 @@
 // every widened value to shared memory and read it back, 640 bytes a token against the 200 that
 // are stored, which alone takes longer than the cache's bytes.
 //
-// Keys in 4 bits: w & 0x0f0f0f0f are four e4m3 values c 2^-9 (subnormals and the first binade are
-// one linear run), which the tensor cores multiply exactly: no conversion.  A query is the sum of
-// two e4m3 values, exactly where it is at least 2^-9 of its row's largest and within 2^-18 of that
-// elsewhere (rows are scaled by powers of two).  The e4m3 MMA (K = 32, one group) takes 4.3 cycles
-// a warp against 8.1 of the 16-bit one with half the K.  A group's (s, z) come in behind
+// Keys in 4 bits: w & 0x000f000f and w & 0x00f000f0 are pairs of f16 subnormals c 2^-24 and
+// c 2^-20, which the tensor cores multiply exactly: no conversion.  The queries of the latter are
+// divided by 16, and every query row is scaled by a power of two so that f16 holds it.  (The e4m3
+// MMA would take the nibbles as they are too, but on sm_100 it is carried out as conversions and
+// 16-bit MMAs: 781 us instead of TIME for 32 sequences of 64K tokens.)  A group's (s, z) come in behind
 // the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as one more MMA with
 // the stored pairs as A and the groups' query sums (two bf16 terms, 2^-18) as B.
 //
-// Values in 4 bits: w & 0x000f000f and w & 0x00f000f0 are pairs of f16 subnormals c 2^-24 and
-// c 2^-20, multiplied exactly as well.  A token's weight is P s 2^k in f16 (one rounding, 2^-11),
+// Values in 4 bits: the same pairs of subnormals, by two tokens of a dim.  A token's weight is P s 2^k in f16 (one rounding, 2^-11),
 // k by group from the largest s met so far, so that weights stay below 2^15; weights below 2^-40 of
 // that limit vanish.  P (z - 8 s) is summed in fp32.  The tensor cores cut off sums instead
 // of rounding them (measured: 4096 steps lose 2e-4), so every 32 tiles the offset's sum is taken into
@@ -48,11 +47,20 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// D = A B
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -68,17 +76,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-// two fp32 values as e4m3 (low byte first), and back
-__device__ __forceinline__ uint32_t to_e4m3(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 from_e4m3(uint32_t x) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -173,12 +170,23 @@ struct Stage {
   static constexpr int kRowKs = INT4 ? DK / 8 : 0, kRowVs = INT4 ? DV / 8 : 0;
   static constexpr int kV = kTile * kRowK, kKs = kV + kTile * kRowV, kVs = kKs + kTile * kRowKs;
   static constexpr int kBytes = kVs + kTile * kRowVs;
-  __device__ static int key_unit(int row, int u) { return INT4 ? u : u ^ ((row & 1) << 2); }
+  __device__ static int key_unit(int row, int u) { return u ^ ((row & 1) << 2); }   // bf16
   __device__ static int value_unit(int row, int u) {
     if constexpr (INT4) return DV == 128 ? u ^ ((row >> 1) & 3) : u;
     return u ^ (((row >> 1) & 3) << 1);
   }
 };
+
+// 16 rows of ROW bytes that lie one behind the other, into the stage as they are; FULL: no row is left out
+template <int ROW, bool FULL>
+__device__ __forceinline__ void copy_run(uint32_t dst, const char* src, int lane, int lo, int hi) {
+  constexpr int kBytes = ROW % 16 == 0 ? 16 : 8, kAll = kTile * ROW / kBytes;
+#pragma unroll
+  for (int i = 0; i < (kAll + 31) / 32; ++i) {
+    const int x = (lane + 32 * i) * kBytes;
+    if (kAll % 32 == 0 || lane + 32 * i < kAll) copy_async<kBytes>(dst + x, src + x, FULL || (x / ROW >= lo && x / ROW < hi));
+  }
+}
 
 // rows [0, 16) of ROW bytes, `stride` apart in memory, into the stage; FULL: no row is left out
 template <int ROW, bool FULL, class Unit>
@@ -198,16 +206,15 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const char* src, size_t 
 template <bool INT4, int DK, int DV, bool FULL>
 __device__ __forceinline__ void copy_tile(const CacheArgs& c, uint32_t dst, int page, int off, int h, int lane, int lo, int hi) {
   using T = Stage<INT4, DK, DV>;
-  const auto ku = [](int r, int u) { return T::key_unit(r, u); };
+  [[maybe_unused]] const auto ku = [](int r, int u) { return T::key_unit(r, u); };
   const auto vu = [](int r, int u) { return T::value_unit(r, u); };
-  const auto same = [](int, int u) { return u; };
   const char *k = static_cast<const char*>(c.k), *v = static_cast<const char*>(c.v);
   if constexpr (INT4) {
     const size_t row = ((size_t)page * c.h_kv + h) * c.page_size + off;
-    copy_rows<T::kRowK, FULL>(dst, k + row * T::kRowK, T::kRowK, lane, lo, hi, ku);
+    copy_run<T::kRowK, FULL>(dst, k + row * T::kRowK, lane, lo, hi);
     copy_rows<T::kRowV, FULL>(dst + T::kV, v + row * T::kRowV, T::kRowV, lane, lo, hi, vu);
-    copy_rows<T::kRowKs, FULL>(dst + T::kKs, static_cast<const char*>(c.k_scale) + row * T::kRowKs, T::kRowKs, lane, lo, hi, same);
-    copy_rows<T::kRowVs, FULL>(dst + T::kVs, static_cast<const char*>(c.v_scale) + row * T::kRowVs, T::kRowVs, lane, lo, hi, same);
+    copy_run<T::kRowKs, FULL>(dst + T::kKs, static_cast<const char*>(c.k_scale) + row * T::kRowKs, lane, lo, hi);
+    copy_run<T::kRowVs, FULL>(dst + T::kVs, static_cast<const char*>(c.v_scale) + row * T::kRowVs, lane, lo, hi);
   } else {
     const size_t row = ((size_t)page * c.page_size + off) * c.h_kv + h;
     copy_rows<T::kRowK, FULL>(dst, k + row * T::kRowK, (size_t)c.h_kv * T::kRowK, lane, lo, hi, ku);
@@ -315,7 +322,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 
     // ---- queries as B fragments: row n = lane / 4 of each tile of 8
     uint32_t qf[NT][KS][2];
-    uint32_t qz[INT4 ? NT : 1][2][2];   // 4 bits: (-8 sum, sum) of the queries of groups q4 and q4 + 4, two terms
+    uint32_t qz[INT4 ? NT : 1][2][2];   // 4 bits: (-8 sum, sum) of the queries of groups, two terms
     float sc[NT][2];                    // what a column's raw score is multiplied by (natural units)
     int pos[NT][2];                     // the columns' positions
     float slope[EXT ? NT : 1][2];
@@ -346,10 +353,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         }
         amax = warp_max4(amax);
         odd = warp_sum4(odd);
-        // a power of two that takes the row's largest query into [2^7, 2^8)
-        const int e2 = min(max(7 - ((int)((__float_as_uint(amax) >> 23) & 255u) - 127), -120), 120);
+        // a power of two that takes the row's largest query into [2^13, 2^14)
+        const int e2 = min(max(13 - ((int)((__float_as_uint(amax) >> 23) & 255u) - 127), -120), 120);
         const float up = pow2(e2);
-        float hi_sum[2] = {0.f, 0.f};
+        float sums[2] = {0.f, 0.f};   // of groups q4 and q4 + 4
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
           const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
@@ -361,23 +368,26 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) sum += x[e];
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {   // even dims, odd dims: the first term and what it leaves
-            const uint32_t t0 = to_e4m3(x[o], x[o + 2]), t1 = to_e4m3(x[o + 4], x[o + 6]);
-            const float2 f0 = from_e4m3(t0), f1 = from_e4m3(t1);
-            qf[nt][2 * gr][o] = t0 | t1 << 16;
-            qf[nt][2 * gr + 1][o] = to_e4m3(x[o] - f0.x, x[o + 2] - f0.y) | to_e4m3(x[o + 4] - f1.x, x[o + 6] - f1.y) << 16;
-          }
-          sum = warp_sum4(sum) * 0x1p-9f;   // the products carry 2^-9: so do the sums beside them
-          if (gr % 4 == q4) hi_sum[gr / 4] = sum;
+          qf[nt][2 * gr][0] = pack_f16(x[0], x[4]);
+          qf[nt][2 * gr][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
+          qf[nt][2 * gr + 1][0] = pack_f16(x[2], x[6]);
+          qf[nt][2 * gr + 1][1] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
+          sum = warp_sum4(sum) * 0x1p-24f;   // the products carry 2^-24: so do the sums beside them
+          if (gr % 4 == q4) sums[gr / 4] = sum;
         }
+        uint32_t term[2][2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float top = __bfloat162float(__float2bfloat16_rn(hi_sum[x])), rest = hi_sum[x] - top;
-          qz[nt][0][x] = pack_bf16(-8.f * top, top);
-          qz[nt][1][x] = pack_bf16(-8.f * rest, rest);
+          const float top = __bfloat162float(__float2bfloat16_rn(sums[x])), rest = sums[x] - top;
+          term[0][x] = pack_bf16(-8.f * top, top);
+          term[1][x] = pack_bf16(-8.f * rest, rest);
         }
-        const float f = fminf(a.scale * pow2(-e2) * 512.f, 1e38f) + odd;
+        // up to four groups: both terms stand side by side in one MMA's K
+        qz[nt][0][0] = term[0][0];
+        qz[nt][0][1] = NG <= 4 ? term[1][0] : term[0][1];
+        qz[nt][1][0] = term[1][0];
+        qz[nt][1][1] = term[1][1];
+        const float f = fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f) + odd;
         sc[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
         sc[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
       }
@@ -473,10 +483,6 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 
       // ---- S = K Q^T
       float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
       if constexpr (INT4) {
         uint32_t kw[2][NG], ks[2][NG], kz[4];
 #pragma unroll
@@ -485,23 +491,25 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           lds_words<NG>(ks[j], st + T::kKs + (g8 + 8 * j) * T::kRowKs);
           const char* row = st + T::kKs + (g8 + 8 * j) * T::kRowKs + q4 * 4;
           kz[j] = NG >= 4 || q4 < NG ? *reinterpret_cast<const uint32_t*>(row) : 0u;
-          kz[j + 2] = q4 + 4 < NG ? *reinterpret_cast<const uint32_t*>(row + 16) : 0u;
+          if constexpr (NG > 4) kz[j + 2] = q4 + 4 < NG ? *reinterpret_cast<const uint32_t*>(row + 16) : 0u;
+          else kz[j + 2] = kz[j];
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_bf16(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][0][0], qz[nt][0][1]);
-          mma_bf16(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][1][0], qz[nt][1][1]);
+          mma_bf16_first(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][0][0], qz[nt][0][1]);
+          if constexpr (NG > 4) mma_bf16(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][1][0], qz[nt][1][1]);
         }
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          const uint32_t w0 = kw[0][gr], w1 = kw[1][gr];
-          const uint32_t e0 = w0 & 0x0f0f0f0fu, e1 = w1 & 0x0f0f0f0fu, o0 = w0 >> 4 & 0x0f0f0f0fu, o1 = w1 >> 4 & 0x0f0f0f0fu;
+          const uint32_t w0 = kw[0][gr], w1 = kw[1][gr], x0 = w0 >> 8, x1 = w1 >> 8;
           const float s0 = cache::bf16_lo(ks[0][gr]), s1 = cache::bf16_lo(ks[1][gr]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_e4m3(acc, e0, e1, o0, o1, qf[nt][2 * gr][0], qf[nt][2 * gr][1]);
-            mma_e4m3(acc, e0, e1, o0, o1, qf[nt][2 * gr + 1][0], qf[nt][2 * gr + 1][1]);
+            float acc[4];
+            mma_f16_first(acc, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][2 * gr][0],
+                          qf[nt][2 * gr][1]);
+            mma_f16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[nt][2 * gr + 1][0],
+                    qf[nt][2 * gr + 1][1]);
             s[nt][0] = fmaf(s0, acc[0], s[nt][0]);
             s[nt][1] = fmaf(s0, acc[1], s[nt][1]);
             s[nt][2] = fmaf(s1, acc[2], s[nt][2]);
@@ -516,7 +524,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           const uint4 k1 = *reinterpret_cast<const uint4*>(st + (g8 + 8) * T::kRowK + x);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16(s[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+            if (i == 0) mma_bf16_first(s[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][0][0], qf[nt][0][1]);
+            else mma_bf16(s[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
             mma_bf16(s[nt], k0.z, k1.z, k0.w, k1.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
           }
         }
