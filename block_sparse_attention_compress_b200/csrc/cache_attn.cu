@@ -77,10 +77,16 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// (x, y) += (a, b) * f and (x, y) * f, as one packed instruction each
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float f) {
+  const float2 r = f2_unpack(f2_fma(f2_pack(a, b), f2_pack(f, f), f2_pack(x, y)));
+  x = r.x;
+  y = r.y;
+}
+__device__ __forceinline__ float2 mul2(float a, float b, float f) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_pack(a, b)), "l"(f2_pack(f, f)));
+  return f2_unpack(d);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
 
@@ -146,19 +152,21 @@ struct Cut {
 struct Span {
   int p0, lo, hi, base, tiles;
 };
+template <int STEP>
 __device__ __forceinline__ Span span_of(int len, int n_new, int i0, int i1, int window) {
   Span s;
   s.p0 = len - n_new;
   s.hi = max(0, s.p0 + i1 + 1);
   s.lo = window > 0 ? max(0, s.p0 + i0 - window + 1) : 0;
   s.base = s.lo & ~(kTile - 1);
-  s.tiles = max(1, (s.hi - s.base + kTile - 1) / kTile);
+  s.tiles = max(1, (s.hi - s.base + STEP - 1) / STEP);
   return s;
 }
+template <int STEP>
 __device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, int b, int rt) {
   const int len = min(max(__ldg(a.seqlens + b), 0), a.max_seqlen);
   const int r0 = rt * p.tile_rows, r1 = min(a.n_new * a.G, r0 + p.tile_rows);
-  return span_of(len, a.n_new, r0 / a.G, (r1 - 1) / a.G, a.window);
+  return span_of<STEP>(len, a.n_new, r0 / a.G, (r1 - 1) / a.G, a.window);
 }
 
 // One tile of 16 tokens as a stage of the ring holds it.  4 bits: key codes, value codes, (s, z) pairs of
@@ -177,64 +185,94 @@ struct Stage {
   }
 };
 
-// 16 rows of ROW bytes that lie one behind the other, into the stage as they are; FULL: no row is left out
-template <int ROW, bool FULL>
-__device__ __forceinline__ void copy_run(uint32_t dst, const char* src, int lane, int lo, int hi) {
+// 16 rows of ROW bytes that lie one behind the other, from the lane's place `src` on, to `at`(x) for unit x;
+// FULL: no row is left out
+template <int ROW, bool FULL, class At>
+__device__ __forceinline__ void copy_run(const char* src, int lane, int lo, int hi, At at) {
   constexpr int kBytes = ROW % 16 == 0 ? 16 : 8, kAll = kTile * ROW / kBytes;
 #pragma unroll
   for (int i = 0; i < (kAll + 31) / 32; ++i) {
-    const int x = (lane + 32 * i) * kBytes;
-    if (kAll % 32 == 0 || lane + 32 * i < kAll) copy_async<kBytes>(dst + x, src + x, FULL || (x / ROW >= lo && x / ROW < hi));
+    const int x = lane + 32 * i, row = x * kBytes / ROW;
+    if (kAll % 32 == 0 || x < kAll) copy_async<kBytes>(at(x), src + 32 * i * kBytes, FULL || (row >= lo && row < hi));
   }
 }
 
-// rows [0, 16) of ROW bytes, `stride` apart in memory, into the stage; FULL: no row is left out
+// rows [0, 16) of ROW bytes, `stride` apart in memory
 template <int ROW, bool FULL, class Unit>
 __device__ __forceinline__ void copy_rows(uint32_t dst, const char* src, size_t stride, int lane, int lo, int hi, Unit unit) {
-  constexpr int kBytes = ROW % 16 == 0 ? 16 : 8, kUnits = ROW / kBytes, kAll = kTile * kUnits;
+  constexpr int kUnits = ROW / 16, kAll = kTile * kUnits;
 #pragma unroll
-  for (int i = 0; i < (kAll + 31) / 32; ++i) {
-    const int x = lane + 32 * i;
-    if (kAll % 32 == 0 || x < kAll) {
-      const int row = x / kUnits, u = x % kUnits;
-      copy_async<kBytes>(dst + row * ROW + unit(row, u) * kBytes, src + row * stride + u * kBytes,
-                         FULL || (row >= lo && row < hi));
+  for (int i = 0; i < kAll / 32; ++i) {
+    const int x = lane + 32 * i, row = x / kUnits, u = x % kUnits;
+    copy_async<16>(dst + row * ROW + unit(row, u) * 16, src + row * stride + u * 16, FULL || (row >= lo && row < hi));
+  }
+}
+
+// Where the tiles of one head lie in memory, walked from tile to tile (4 bits: a lane's own places, so that a
+// copy is an instruction of its own and little else).
+template <bool INT4, int DK, int DV>
+struct Walk {
+  using T = Stage<INT4, DK, DV>;
+  const char *k, *v, *ks, *vs;
+  __device__ __forceinline__ void go(const CacheArgs& c, int page, int off, int h, int lane) {
+    if constexpr (INT4) {
+      const size_t row = ((size_t)page * c.h_kv + h) * c.page_size + off;
+      k = static_cast<const char*>(c.k) + row * T::kRowK + lane * 16;
+      v = static_cast<const char*>(c.v) + row * T::kRowV + lane * 16;
+      ks = static_cast<const char*>(c.k_scale) + row * T::kRowKs + lane * (T::kRowKs % 16 ? 8 : 16);
+      vs = static_cast<const char*>(c.v_scale) + row * T::kRowVs + lane * (T::kRowVs % 16 ? 8 : 16);
+    } else {
+      const size_t row = ((size_t)page * c.page_size + off) * c.h_kv + h;
+      k = static_cast<const char*>(c.k) + row * T::kRowK;
+      v = static_cast<const char*>(c.v) + row * T::kRowV;
     }
   }
-}
-
-template <bool INT4, int DK, int DV, bool FULL>
-__device__ __forceinline__ void copy_tile(const CacheArgs& c, uint32_t dst, int page, int off, int h, int lane, int lo, int hi) {
-  using T = Stage<INT4, DK, DV>;
-  [[maybe_unused]] const auto ku = [](int r, int u) { return T::key_unit(r, u); };
-  const auto vu = [](int r, int u) { return T::value_unit(r, u); };
-  const char *k = static_cast<const char*>(c.k), *v = static_cast<const char*>(c.v);
-  if constexpr (INT4) {
-    const size_t row = ((size_t)page * c.h_kv + h) * c.page_size + off;
-    copy_run<T::kRowK, FULL>(dst, k + row * T::kRowK, lane, lo, hi);
-    copy_rows<T::kRowV, FULL>(dst + T::kV, v + row * T::kRowV, T::kRowV, lane, lo, hi, vu);
-    copy_run<T::kRowKs, FULL>(dst + T::kKs, static_cast<const char*>(c.k_scale) + row * T::kRowKs, lane, lo, hi);
-    copy_run<T::kRowVs, FULL>(dst + T::kVs, static_cast<const char*>(c.v_scale) + row * T::kRowVs, lane, lo, hi);
-  } else {
-    const size_t row = ((size_t)page * c.page_size + off) * c.h_kv + h;
-    copy_rows<T::kRowK, FULL>(dst, k + row * T::kRowK, (size_t)c.h_kv * T::kRowK, lane, lo, hi, ku);
-    copy_rows<T::kRowV, FULL>(dst + T::kV, v + row * T::kRowV, (size_t)c.h_kv * T::kRowV, lane, lo, hi, vu);
+  __device__ __forceinline__ void next(const CacheArgs& c) {   // the next 16 tokens of the page
+    const int n = INT4 ? kTile : kTile * c.h_kv;
+    k += (size_t)n * T::kRowK;
+    v += (size_t)n * T::kRowV;
+    if constexpr (INT4) {
+      ks += n * T::kRowKs;
+      vs += n * T::kRowVs;
+    }
   }
+  template <bool FULL>
+  __device__ __forceinline__ void copy(const CacheArgs& c, uint32_t dst, int lane, int lo, int hi) const {
+    if constexpr (INT4) {
+      copy_run<T::kRowK, FULL>(k, lane, lo, hi, [&](int x) { return dst + x * 16; });
+      copy_run<T::kRowV, FULL>(v, lane, lo, hi, [&](int x) {
+        constexpr int kUnits = T::kRowV / 16;
+        return dst + T::kV + (x / kUnits * kUnits + T::value_unit(x / kUnits, x % kUnits)) * 16;
+      });
+      copy_run<T::kRowKs, FULL>(ks, lane, lo, hi, [&](int x) { return dst + T::kKs + x * (T::kRowKs % 16 ? 8 : 16); });
+      copy_run<T::kRowVs, FULL>(vs, lane, lo, hi, [&](int x) { return dst + T::kVs + x * (T::kRowVs % 16 ? 8 : 16); });
+    } else {
+      copy_rows<T::kRowK, FULL>(dst, k, (size_t)c.h_kv * T::kRowK, lane, lo, hi, [](int r, int u) { return T::key_unit(r, u); });
+      copy_rows<T::kRowV, FULL>(dst + T::kV, v, (size_t)c.h_kv * T::kRowV, lane, lo, hi, [](int r, int u) { return T::value_unit(r, u); });
+    }
+  }
+};
+
+// Shared memory of a block: a ring (and later the joined rows) per warp, then in 4 bits the queries of
+// each row group: per tile of 8 rows the B fragments [DK / 32][32 lanes] x 16 bytes, the group sums'
+// [32 lanes] x 16 bytes and the rows' factors.
+template <bool INT4, int DK, int DV, int NT, int U, int S>
+constexpr int warp_smem() {
+  return std::max(S * U * Stage<INT4, DK, DV>::kBytes, NT * 8 * (DV + 4 + 2) * 4);
+}
+template <bool INT4, int DK, int NT>
+constexpr int query_smem() {
+  return INT4 ? NT * ((DK / 32 + 1) * 512 + 8 * 4) : 0;
 }
 
-template <bool INT4, int DK, int DV, int NT, int W, int S>
-constexpr int attn_smem() {
-  return W * std::max(S * Stage<INT4, DK, DV>::kBytes, NT * 8 * (DV + 4 + 2) * 4);
-}
-
-template <bool INT4, int DK, int DV, int NT, int W, int MINB, int S, bool EXT>
+template <bool INT4, int DK, int DV, int NT, int W, int MINB, int U, int S, bool EXT>
 __global__ void __launch_bounds__(W * 32, MINB)
 cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* __restrict__ cuts, float2* __restrict__ part_ml,
                   float* __restrict__ part_o) {
   using T = Stage<INT4, DK, DV>;
   constexpr int NG = DK / 32, NH = DV / 32, MT = DV / 16, KS = DK / 16;
   constexpr int kCols = NT * 8, kRow = DV + 4;
-  constexpr int kWarpBytes = attn_smem<INT4, DK, DV, NT, W, S>() / W;
+  constexpr int kWarpBytes = warp_smem<INT4, DK, DV, NT, U, S>(), kStep = kTile * U, kQ = query_smem<INT4, DK, NT>();
   extern __shared__ __align__(128) char smem[];
   __shared__ long long s_scan[W];
   __shared__ long long s_off;
@@ -244,6 +282,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   const int R = a.n_new * a.G;
   char* ring = smem + warp * kWarpBytes;
   const uint32_t ring_u = smem_u32(ring);
+  char* sq = smem + W * kWarpBytes + rg * kQ;                     // this row group's queries
+  float* sq_sc = reinterpret_cast<float*>(sq + NT * (NG + 1) * 512);
 
   if (c.status) {   // lengths out of range are told of once
     for (long long b = (long long)blockIdx.x * blockDim.x + threadIdx.x; b < c.batch; b += (long long)gridDim.x * blockDim.x) {
@@ -260,11 +300,11 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     rt = id % pl.row_tiles; id /= pl.row_tiles;
     h = id % c.h_kv;
     b = id / c.h_kv;
-    left = span_of(c, a, pl, b, rt).tiles;
+    left = span_of<kStep>(c, a, pl, b, rt).tiles;
   } else {
     const auto weight = [&](int bb) {
       long long w = 0;
-      for (int x = 0; x < pl.row_tiles; ++x) w += span_of(c, a, pl, bb, x).tiles;
+      for (int x = 0; x < pl.row_tiles; ++x) w += span_of<kStep>(c, a, pl, bb, x).tiles;
       return w * c.h_kv;
     };
     const int strip = (c.batch + W * 32 - 1) / (W * 32);
@@ -304,13 +344,13 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     h = (int)(s_off / head);
     t = (int)(s_off % head);
     rt = 0;
-    for (int n; t >= (n = span_of(c, a, pl, b, rt).tiles); ++rt) t -= n;
+    for (int n; t >= (n = span_of<kStep>(c, a, pl, b, rt).tiles); ++rt) t -= n;
     left = min(per, total - pos0);
   }
 
   Cut cut{0, 0, -1, 0};
   while (left > 0) {
-    const Span sp = span_of(c, a, pl, b, rt);
+    const Span sp = span_of<kStep>(c, a, pl, b, rt);
     const int take = (int)min(left, (long long)(sp.tiles - t));
     const int r0 = rt * pl.tile_rows + rg * kCols;   // this warp's first row (maybe behind the last)
     if (t == 0 && take < sp.tiles) {
@@ -320,85 +360,84 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       cut.rows = min(R - rt * pl.tile_rows, pl.tile_rows);
     }
 
-    // ---- queries as B fragments: row n = lane / 4 of each tile of 8
-    uint32_t qf[NT][KS][2];
-    uint32_t qz[INT4 ? NT : 1][2][2];   // 4 bits: (-8 sum, sum) of the queries of groups, two terms
+    // ---- queries as B fragments: row n = lane / 4 of each tile of 8.  4 bits: through shared memory
+    uint32_t qf[INT4 ? 1 : NT][INT4 ? 1 : KS][2];
     float sc[NT][2];                    // what a column's raw score is multiplied by (natural units)
     int pos[NT][2];                     // the columns' positions
     float slope[EXT ? NT : 1][2];
+    if (!INT4 || ts == 0) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = min(r0 + nt * 8 + g8, R - 1), i = r / a.G, g = r - i * a.G;
-      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
-      if constexpr (!INT4) {
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = min(r0 + nt * 8 + g8, R - 1), i = r / a.G, g = r - i * a.G;
+        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
+        if constexpr (!INT4) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
-          qf[nt][ks][0] = u.x;
-          qf[nt][ks][1] = u.y;
-        }
-        sc[nt][0] = sc[nt][1] = a.scale;
-      } else {
-        uint4 u[NG];
-        float amax = 0.f, odd = 0.f;   // odd: NaN as soon as one query is not finite
-#pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
-          const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            amax = fmaxf(amax, fmaxf(fabsf(cache::bf16_lo(w[e])), fabsf(cache::bf16_hi(w[e]))));
-            odd = fmaf(cache::bf16_lo(w[e]), 0.f, fmaf(cache::bf16_hi(w[e]), 0.f, odd));
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
+            qf[nt][ks][0] = u.x;
+            qf[nt][ks][1] = u.y;
           }
-        }
-        amax = warp_max4(amax);
-        odd = warp_sum4(odd);
-        // a power of two that takes the row's largest query into [2^13, 2^14)
-        const int e2 = min(max(13 - ((int)((__float_as_uint(amax) >> 23) & 255u) - 127), -120), 120);
-        const float up = pow2(e2);
-        float sums[2] = {0.f, 0.f};   // of groups q4 and q4 + 4
+        } else {
+          uint4 u[NG];
+          float amax = 0.f, odd = 0.f;   // odd: NaN as soon as one query is not finite
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
-          float x[8], sum = 0.f;
+          for (int gr = 0; gr < NG; ++gr) {
+            u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
+            const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[2 * e] = cache::bf16_lo(w[e]) * up;
-            x[2 * e + 1] = cache::bf16_hi(w[e]) * up;
+            for (int e = 0; e < 4; ++e) {
+              amax = fmaxf(amax, fmaxf(fabsf(cache::bf16_lo(w[e])), fabsf(cache::bf16_hi(w[e]))));
+              odd = fmaf(cache::bf16_lo(w[e]), 0.f, fmaf(cache::bf16_hi(w[e]), 0.f, odd));
+            }
           }
+          amax = warp_max4(amax);
+          odd = warp_sum4(odd);
+          // a power of two that takes the row's largest query into [2^13, 2^14)
+          const int e2 = min(max(13 - ((int)((__float_as_uint(amax) >> 23) & 255u) - 127), -120), 120);
+          const float up = pow2(e2);
+          float sums[2] = {0.f, 0.f};   // of groups q4 and q4 + 4
+          uint4* frag = reinterpret_cast<uint4*>(sq) + nt * (NG + 1) * 32 + lane;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum += x[e];
-          qf[nt][2 * gr][0] = pack_f16(x[0], x[4]);
-          qf[nt][2 * gr][1] = pack_f16(x[1] * 0.0625f, x[5] * 0.0625f);
-          qf[nt][2 * gr + 1][0] = pack_f16(x[2], x[6]);
-          qf[nt][2 * gr + 1][1] = pack_f16(x[3] * 0.0625f, x[7] * 0.0625f);
-          sum = warp_sum4(sum) * 0x1p-24f;   // the products carry 2^-24: so do the sums beside them
-          if (gr % 4 == q4) sums[gr / 4] = sum;
-        }
-        uint32_t term[2][2];
+          for (int gr = 0; gr < NG; ++gr) {
+            const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
+            float x[8], sum = 0.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const float top = __bfloat162float(__float2bfloat16_rn(sums[x])), rest = sums[x] - top;
-          term[0][x] = pack_bf16(-8.f * top, top);
-          term[1][x] = pack_bf16(-8.f * rest, rest);
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = cache::bf16_lo(w[e]) * up;
+              x[2 * e + 1] = cache::bf16_hi(w[e]) * up;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += x[e];
+            frag[gr * 32] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1] * 0.0625f, x[5] * 0.0625f), pack_f16(x[2], x[6]),
+                                       pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
+            sum = warp_sum4(sum) * 0x1p-24f;   // the products carry 2^-24: so do the sums beside them
+            if (gr % 4 == q4) sums[gr / 4] = sum;
+          }
+          // (-8 sum, sum) of the groups' queries, each in two terms: one MMA's K holds eight groups' first
+          // terms and a second one the rest, or both terms of up to four groups
+          uint32_t term[2][2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float top = __bfloat162float(__float2bfloat16_rn(sums[x])), rest = sums[x] - top;
+            term[0][x] = pack_bf16(-8.f * top, top);
+            term[1][x] = pack_bf16(-8.f * rest, rest);
+          }
+          frag[NG * 32] = make_uint4(term[0][0], NG <= 4 ? term[1][0] : term[0][1], term[1][0], term[1][1]);
+          if (q4 == 0) sq_sc[nt * 8 + g8] = fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f) + odd;
         }
-        // up to four groups: both terms stand side by side in one MMA's K
-        qz[nt][0][0] = term[0][0];
-        qz[nt][0][1] = NG <= 4 ? term[1][0] : term[0][1];
-        qz[nt][1][0] = term[1][0];
-        qz[nt][1][1] = term[1][1];
-        const float f = fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f) + odd;
-        sc[nt][0] = __shfl_sync(0xffffffffu, f, 8 * q4);
-        sc[nt][1] = __shfl_sync(0xffffffffu, f, 8 * q4 + 4);
       }
+    }
+    if constexpr (INT4) __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int rc = min(r0 + nt * 8 + 2 * q4 + j, R - 1), ic = rc / a.G;
+        sc[nt][j] = INT4 ? sq_sc[nt * 8 + 2 * q4 + j] : a.scale;
         pos[nt][j] = sp.p0 + ic;
         if constexpr (EXT) slope[nt][j] = a.slopes ? __ldg(a.slopes + h * a.G + rc - ic * a.G) * kLog2e : 0.f;
         else sc[nt][j] *= kLog2e;
       }
-    }
 
     float o[MT][NT][4];
     float m[NT][2], l[NT][2], zacc[INT4 ? NT : 1][NH][2];
@@ -431,38 +470,56 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     // ---- this warp's run of tiles, [ta, tb) of the item
     const int each = (take + streams - 1) / streams;
     const int ta = t + min(take, ts * each), tb = t + min(take, (ts + 1) * each);
-    // tiles inside [all_lo, all_hi) are seen whole by every row of the block
+    // steps inside [all_lo, all_hi) are seen whole by every row of the block
     const int row_lo = rt * pl.tile_rows / a.G, row_hi = (min(R, (rt + 1) * pl.tile_rows) - 1) / a.G;
     const int all_lo = a.window > 0 ? max(0, sp.p0 + row_hi - a.window + 1) : 0, all_hi = sp.p0 + row_lo + 1;
 
-    // the place of the next tile to copy; its page is fetched one tile ahead
-    int cp_t = ta, cp_j = 0, cp_off = 0, cp_page = -1;
-    uint32_t missing = 0;   // stages whose tile has no valid page
+    // the next tile to copy: its place in its page, and the page after that one, fetched ahead
+    int cp_u = sp.base + ta * kStep, cp_j = 0, cp_off = 0, ahead = 0;
+    const int cp_end = sp.base + tb * kStep;
+    bool here = false;      // the page is valid
+    uint32_t missing = 0;   // bit stage * U + x: tile x of that stage has no valid page
     const int32_t* pages = c.page_table + (size_t)b * c.max_pages;
-    if (ta < tb) {
-      const int u = sp.base + ta * kTile;
-      cp_j = u / c.page_size;
-      cp_off = u - cp_j * c.page_size;
-      if (sp.hi > 0) cp_page = __ldg(pages + cp_j);
+    Walk<INT4, DK, DV> walk;
+    const auto open_page = [&](int page) {
+      here = page >= 0 && page < c.n_pages;
+      walk.go(c, here ? page : 0, cp_off, h, lane);
+      if (!here && lane == 0) cache::report(c.status);
+      // pages behind the last token are not looked up
+      const long long next = (long long)(cp_j + 1) * c.page_size;
+      ahead = next < min(sp.hi, cp_end) ? __ldg(pages + cp_j + 1) : -1;
+    };
+    if (ta < tb && sp.hi > 0) {
+      cp_j = cp_u / c.page_size;
+      cp_off = cp_u - cp_j * c.page_size;
+      open_page(__ldg(pages + cp_j));
+    } else {
+      walk.go(c, 0, 0, h, lane);
     }
     const auto copy_next = [&](int stage) {
-      if (cp_t < tb) {
-        const int u0 = sp.base + cp_t * kTile, lo = sp.lo - u0, hi = sp.hi - u0;
-        const uint32_t dst = ring_u + stage * T::kBytes;
-        if (cp_page >= 0 && cp_page < c.n_pages) {
-          missing &= ~(1u << stage);
-          if (lo <= 0 && hi >= kTile) copy_tile<INT4, DK, DV, true>(c, dst, cp_page, cp_off, h, lane, 0, kTile);
-          else copy_tile<INT4, DK, DV, false>(c, dst, cp_page, cp_off, h, lane, lo, hi);
-        } else {
-          missing |= 1u << stage;
-          if (lane == 0 && hi > 0) cache::report(c.status);
-        }
-        ++cp_t;
-        cp_off += kTile;
-        if (cp_off >= c.page_size) {
-          cp_off = 0;
-          ++cp_j;
-          if (cp_t < tb) cp_page = __ldg(pages + cp_j);
+      if (cp_u < cp_end) {
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          const uint32_t dst = ring_u + (stage * U + x) * T::kBytes, bit = 1u << (stage * U + x);
+          if (here && cp_u >= sp.lo && cp_u + kTile <= sp.hi) {
+            walk.template copy<true>(c, dst, lane, 0, kTile);
+            missing &= ~bit;
+          } else {   // rows that do not exist are zeros, and masked
+            const bool some = here && cp_u < sp.hi;
+            walk.template copy<false>(c, dst, lane, some ? sp.lo - cp_u : 0, some ? sp.hi - cp_u : 0);
+            missing = some ? missing & ~bit : missing | bit;
+          }
+          cp_u += kTile;
+          cp_off += kTile;
+          if (cp_off < c.page_size) {
+            walk.next(c);
+          } else if (cp_u < min(sp.hi, cp_end)) {
+            cp_off = 0;
+            ++cp_j;
+            open_page(ahead);
+          } else {
+            here = false;
+          }
         }
       }
       cp_async_commit();
@@ -474,113 +531,136 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     for (int tile = ta; tile < tb; ++tile) {
       cp_async_wait<S - 2>();
       __syncwarp();
-      const bool gone = missing >> stage & 1;
+      const uint32_t gone = missing >> (stage * U) & ((1u << U) - 1);
       copy_next(stage == 0 ? S - 1 : stage - 1);
-      const char* st = ring + stage * T::kBytes;
+      const char* st = ring + stage * U * T::kBytes;
       stage = stage == S - 1 ? 0 : stage + 1;
-      if (gone) continue;
-      const int u0 = sp.base + tile * kTile;
+      const int u0 = sp.base + tile * kStep;
 
       // ---- S = K Q^T
-      float s[NT][4];
+      float s[U][NT][4];
       if constexpr (INT4) {
-        uint32_t kw[2][NG], ks[2][NG], kz[4];
+        uint4 q[NT];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          lds_words<NG>(kw[j], st + (g8 + 8 * j) * T::kRowK + q4 * (NG * 4));
-          lds_words<NG>(ks[j], st + T::kKs + (g8 + 8 * j) * T::kRowKs);
-          const char* row = st + T::kKs + (g8 + 8 * j) * T::kRowKs + q4 * 4;
-          kz[j] = NG >= 4 || q4 < NG ? *reinterpret_cast<const uint32_t*>(row) : 0u;
-          if constexpr (NG > 4) kz[j + 2] = q4 + 4 < NG ? *reinterpret_cast<const uint32_t*>(row + 16) : 0u;
-          else kz[j + 2] = kz[j];
-        }
+        for (int nt = 0; nt < NT; ++nt) q[nt] = *reinterpret_cast<const uint4*>(sq + (nt * (NG + 1) + NG) * 512 + lane * 16);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_bf16_first(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][0][0], qz[nt][0][1]);
-          if constexpr (NG > 4) mma_bf16(s[nt], kz[0], kz[1], kz[2], kz[3], qz[nt][1][0], qz[nt][1][1]);
-        }
+        for (int x = 0; x < U; ++x) {
+          uint32_t kz[4];
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
-          const uint32_t w0 = kw[0][gr], w1 = kw[1][gr], x0 = w0 >> 8, x1 = w1 >> 8;
-          const float s0 = cache::bf16_lo(ks[0][gr]), s1 = cache::bf16_lo(ks[1][gr]);
+          for (int j = 0; j < 2; ++j) {
+            const char* row = st + x * T::kBytes + T::kKs + (g8 + 8 * j) * T::kRowKs + q4 * 4;
+            kz[j] = NG >= 4 || q4 < NG ? *reinterpret_cast<const uint32_t*>(row) : 0u;
+            if constexpr (NG > 4) kz[j + 2] = q4 + 4 < NG ? *reinterpret_cast<const uint32_t*>(row + 16) : 0u;
+            else kz[j + 2] = kz[j];
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4];
-            mma_f16_first(acc, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, qf[nt][2 * gr][0],
-                          qf[nt][2 * gr][1]);
-            mma_f16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[nt][2 * gr + 1][0],
-                    qf[nt][2 * gr + 1][1]);
-            s[nt][0] = fmaf(s0, acc[0], s[nt][0]);
-            s[nt][1] = fmaf(s0, acc[1], s[nt][1]);
-            s[nt][2] = fmaf(s1, acc[2], s[nt][2]);
-            s[nt][3] = fmaf(s1, acc[3], s[nt][3]);
+            mma_bf16_first(s[x][nt], kz[0], kz[1], kz[2], kz[3], q[nt].x, q[nt].y);
+            if constexpr (NG > 4) mma_bf16(s[x][nt], kz[0], kz[1], kz[2], kz[3], q[nt].z, q[nt].w);
+          }
+        }
+        constexpr int GC = NG == 4 ? 4 : 2;   // groups whose words a lane loads at once
+#pragma unroll
+        for (int gc = 0; gc < NG; gc += GC) {
+          uint32_t kw[U][2][GC], ks[U][2][GC];
+#pragma unroll
+          for (int x = 0; x < U; ++x)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              lds_words<GC>(kw[x][j], st + x * T::kBytes + (g8 + 8 * j) * T::kRowK + q4 * (NG * 4) + gc * 4);
+              lds_words<GC>(ks[x][j], st + x * T::kBytes + T::kKs + (g8 + 8 * j) * T::kRowKs + gc * 4);
+            }
+#pragma unroll
+          for (int gr = 0; gr < GC; ++gr) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) q[nt] = *reinterpret_cast<const uint4*>(sq + (nt * (NG + 1) + gc + gr) * 512 + lane * 16);
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+              const uint32_t w0 = kw[x][0][gr], w1 = kw[x][1][gr], x0 = w0 >> 8, x1 = w1 >> 8;
+              const float s0 = cache::bf16_lo(ks[x][0][gr]), s1 = cache::bf16_lo(ks[x][1][gr]);
+              float acc[NT][4];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16_first(acc[nt], w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u, q[nt].x, q[nt].y);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16(acc[nt], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q[nt].z, q[nt].w);
+                fma2(s[x][nt][0], s[x][nt][1], acc[nt][0], acc[nt][1], s0);
+                fma2(s[x][nt][2], s[x][nt][3], acc[nt][2], acc[nt][3], s1);
+              }
+            }
           }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < DK / 32; ++i) {
-          const int x = T::key_unit(g8, 4 * i + q4) * 16;   // rows g8 and g8 + 8 turn alike
-          const uint4 k0 = *reinterpret_cast<const uint4*>(st + g8 * T::kRowK + x);
-          const uint4 k1 = *reinterpret_cast<const uint4*>(st + (g8 + 8) * T::kRowK + x);
+        for (int x = 0; x < U; ++x)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (i == 0) mma_bf16_first(s[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][0][0], qf[nt][0][1]);
-            else mma_bf16(s[nt], k0.x, k1.x, k0.y, k1.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
-            mma_bf16(s[nt], k0.z, k1.z, k0.w, k1.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+          for (int i = 0; i < DK / 32; ++i) {
+            const char* row = st + x * T::kBytes + g8 * T::kRowK + T::key_unit(g8, 4 * i + q4) * 16;   // g8 and g8 + 8 turn alike
+            const uint4 k0 = *reinterpret_cast<const uint4*>(row), k1 = *reinterpret_cast<const uint4*>(row + 8 * T::kRowK);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (i == 0) mma_bf16_first(s[x][nt], k0.x, k1.x, k0.y, k1.y, qf[nt][0][0], qf[nt][0][1]);
+              else mma_bf16(s[x][nt], k0.x, k1.x, k0.y, k1.y, qf[nt][2 * i][0], qf[nt][2 * i][1]);
+              mma_bf16(s[x][nt], k0.z, k1.z, k0.w, k1.w, qf[nt][2 * i + 1][0], qf[nt][2 * i + 1][1]);
+            }
           }
-        }
       }
 
       // ---- softmax: scores in log2 units, the reference moved only when a score passes it by 8
-      uint32_t vs[2][INT4 ? NH : 1];
+      uint32_t sv[INT4 ? NH : 1];   // 4 bits: the scales of the values of token `lane` of the step
       bool move = false;
       if constexpr (INT4) {
+        const int tok = lane % kStep;
+        lds_words<NH>(sv, st + (tok / kTile) * T::kBytes + T::kVs + (tok % kTile) * T::kRowVs);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) lds_words<NH>(vs[j], st + T::kVs + (g8 + 8 * j) * T::kRowVs);
-#pragma unroll
-        for (int gr = 0; gr < NH; ++gr) move |= (max_u16x2(vs[0][gr], vs[1][gr]) & 0xffffu) > max_s[gr];
+        for (int gr = 0; gr < NH; ++gr) move |= (sv[gr] & 0xffffu) > max_s[gr];
       }
-      const bool inner = u0 >= all_lo && u0 + kTile <= all_hi;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[nt][e] * sc[nt][e & 1];
-          if constexpr (EXT) {
-            if (a.softcap > 0.f) x = capped(x, a.softcap, a.inv_softcap);
-            x = fmaf(x, kLog2e, slope[nt][e & 1] * (float)(u0 + g8 + 8 * (e >> 1) - pos[nt][e & 1]));
-          }
-          s[nt][e] = x;
-        }
-      if (!inner) {
+      for (int x = 0; x < U; ++x)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int u = u0 + g8 + 8 * (e >> 1), p = pos[nt][e & 1];
-            if (u > p || u < sp.lo || (a.window > 0 && u <= p - a.window)) s[nt][e] = -INFINITY;
+            float y = s[x][nt][e] * sc[nt][e & 1];
+            if constexpr (EXT) {
+              if (a.softcap > 0.f) y = capped(y, a.softcap, a.inv_softcap);
+              y = fmaf(y, kLog2e, slope[nt][e & 1] * (float)(u0 + x * kTile + g8 + 8 * (e >> 1) - pos[nt][e & 1]));
+            }
+            s[x][nt][e] = y;
           }
+      if (gone || u0 < all_lo || u0 + kStep > all_hi) {
+#pragma unroll
+        for (int x = 0; x < U; ++x)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int u = u0 + x * kTile + g8 + 8 * (e >> 1), p = pos[nt][e & 1];
+              if ((gone >> x & 1) || u > p || u < sp.lo || (a.window > 0 && u <= p - a.window)) s[x][nt][e] = -INFINITY;
+            }
       }
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) move |= fmaxf(s[nt][j], s[nt][j + 2]) > m[nt][j] + 8.f;
+        for (int j = 0; j < 2; ++j) {
+          top[nt][j] = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+          for (int x = 1; x < U; ++x) top[nt][j] = fmaxf(top[nt][j], fmaxf(s[x][nt][j], s[x][nt][j + 2]));
+          move |= top[nt][j] > m[nt][j] + 8.f;
+        }
       if (__any_sync(0xffffffffu, move)) {
         float grow[INT4 ? NH : 1];
         if constexpr (INT4) {
 #pragma unroll
           for (int gr = 0; gr < NH; ++gr) {
-            uint32_t x = max_s[gr];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t y = vs[j][gr] & 0xffffu;
-              if (y < 0x7f80u) x = max(x, y);   // a NaN shows in its products
-            }
-            x = __reduce_max_sync(0xffffffffu, x);
+            uint32_t x = sv[gr] & 0xffffu;
+            x = __reduce_max_sync(0xffffffffu, x < 0x7f80u ? x : 0u);   // a NaN shows in its products
+            x = max(x, max_s[gr]);
             x = x ? x | 0x7fu : 0u;             // all of the binade
             // s 2^k < 2^7: k = 6 - (exponent of s)
-            const int k = x ? min(6 - ((int)(x >> 7) - 127), 100) : 100;
-            const float to = pow2(k);
+            const float to = pow2(x ? min(6 - ((int)(x >> 7) - 127), 100) : 100);
             grow[gr] = to / top_s[gr];
             top_s[gr] = to;
             max_s[gr] = x;
@@ -590,7 +670,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float x = fmaxf(s[nt][j], s[nt][j + 2]);
+            float x = top[nt][j];
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
             x = fmaxf(x, m[nt][j]);
@@ -610,47 +690,56 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < U; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float p = ex2(s[nt][e] - m[nt][e & 1]);
-          s[nt][e] = p;
-          l[nt][e & 1] += p;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float p = ex2(s[x][nt][e] - m[nt][e & 1]);
+            s[x][nt][e] = p;
+            l[nt][e & 1] += p;
+          }
 
       // ---- O^T += V^T P^T
       if constexpr (INT4) {
-        uint32_t vw[4][NH / 2];   // tokens 2q, 2q+1, 2q+8, 2q+9
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = 2 * q4 + (j & 1) + 8 * (j >> 1);
-          const int at = g8 * (NH * 2);
-          lds_words<NH / 2>(vw[j], st + T::kV + row * T::kRowV + T::value_unit(row, at / 16) * 16 + at % 16);
-        }
+        for (int x = 0; x < U; ++x) {
+          const char* sx = st + x * T::kBytes;
+          uint32_t vs[2][NH], vw[4][NH / 2];   // rows g8, g8 + 8; tokens 2q, 2q+1, 2q+8, 2q+9
 #pragma unroll
-        for (int gr = 0; gr < NH; ++gr) {
-          uint32_t pb[NT][2];
-          const float r0s = cache::bf16_lo(vs[0][gr]), r1s = cache::bf16_lo(vs[1][gr]);
-          const float s0 = r0s * top_s[gr], s1 = r1s * top_s[gr];
-          const float z0 = fmaf(-8.f, r0s, cache::bf16_hi(vs[0][gr])), z1 = fmaf(-8.f, r1s, cache::bf16_hi(vs[1][gr]));
+          for (int j = 0; j < 2; ++j) lds_words<NH>(vs[j], sx + T::kVs + (g8 + 8 * j) * T::kRowVs);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            pb[nt][0] = movmatrix(pack_f16(s[nt][0] * s0, s[nt][1] * s0));
-            pb[nt][1] = movmatrix(pack_f16(s[nt][2] * s1, s[nt][3] * s1));
-            zacc[nt][gr][0] = fmaf(s[nt][0], z0, fmaf(s[nt][2], z1, zacc[nt][gr][0]));
-            zacc[nt][gr][1] = fmaf(s[nt][1], z0, fmaf(s[nt][3], z1, zacc[nt][gr][1]));
+          for (int j = 0; j < 4; ++j) {
+            const int row = 2 * q4 + (j & 1) + 8 * (j >> 1), at = g8 * (NH * 2);
+            lds_words<NH / 2>(vw[j], sx + T::kV + row * T::kRowV + T::value_unit(row, at / 16) * 16 + at % 16);
           }
-          const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
-          const uint32_t lo = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel), lo8 = lo >> 8;
-          const uint32_t hi = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel), hi8 = hi >> 8;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16(o[2 * gr][nt], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, pb[nt][0], pb[nt][1]);
-            mma_f16(o[2 * gr + 1][nt], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, pb[nt][0],
-                    pb[nt][1]);
+          for (int gr = 0; gr < NH; ++gr) {
+            uint32_t pb[NT][2];
+            const float r0s = cache::bf16_lo(vs[0][gr]), r1s = cache::bf16_lo(vs[1][gr]);
+            const float s0 = r0s * top_s[gr], s1 = r1s * top_s[gr];
+            const float z0 = fmaf(-8.f, r0s, cache::bf16_hi(vs[0][gr])), z1 = fmaf(-8.f, r1s, cache::bf16_hi(vs[1][gr]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float(&p)[4] = s[x][nt];
+              const float2 w0 = mul2(p[0], p[1], s0), w1 = mul2(p[2], p[3], s1);
+              pb[nt][0] = movmatrix(pack_f16(w0.x, w0.y));
+              pb[nt][1] = movmatrix(pack_f16(w1.x, w1.y));
+              fma2(zacc[nt][gr][0], zacc[nt][gr][1], p[0], p[1], z0);
+              fma2(zacc[nt][gr][0], zacc[nt][gr][1], p[2], p[3], z1);
+            }
+            const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
+            const uint32_t lo = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel), lo8 = lo >> 8;
+            const uint32_t hi = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel), hi8 = hi >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(o[2 * gr][nt], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, pb[nt][0], pb[nt][1]);
+              mma_f16(o[2 * gr + 1][nt], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, pb[nt][0],
+                      pb[nt][1]);
+            }
           }
         }
-        if (++since == kFlush) {   // take the offset's sum into the accumulators
+        if (++since == kFlush / U) {   // take the offset's sum into the accumulators
           since = 0;
 #pragma unroll
           for (int gr = 0; gr < NH; ++gr)
@@ -672,27 +761,30 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
               }
         }
       } else {
-        uint32_t pb[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          pb[nt][0] = movmatrix(pack_bf16(s[nt][0], s[nt][1]));
-          pb[nt][1] = movmatrix(pack_bf16(s[nt][2], s[nt][3]));
-        }
-        const char* vrow = st + T::kV + 2 * q4 * T::kRowV;
+        for (int x = 0; x < U; ++x) {
+          uint32_t pb[NT][2];
 #pragma unroll
-        for (int i = 0; i < DV / 64; ++i) {
-          const int x = T::value_unit(2 * q4, 8 * i + g8) * 16;   // the lane's four rows turn alike
-          const uint4 v0 = *reinterpret_cast<const uint4*>(vrow + x), v1 = *reinterpret_cast<const uint4*>(vrow + T::kRowV + x);
-          const uint4 v2 = *reinterpret_cast<const uint4*>(vrow + 8 * T::kRowV + x);
-          const uint4 v3 = *reinterpret_cast<const uint4*>(vrow + 9 * T::kRowV + x);
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-          const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+          for (int nt = 0; nt < NT; ++nt) {
+            pb[nt][0] = movmatrix(pack_bf16(s[x][nt][0], s[x][nt][1]));
+            pb[nt][1] = movmatrix(pack_bf16(s[x][nt][2], s[x][nt][3]));
+          }
+          const char* vrow = st + x * T::kBytes + T::kV + 2 * q4 * T::kRowV;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)   // word e holds dims 2 e and 2 e + 1 of the lane's eight
+          for (int i = 0; i < DV / 64; ++i) {
+            const int at = T::value_unit(2 * q4, 8 * i + g8) * 16;   // the lane's four rows turn alike
+            const uint4 v0 = *reinterpret_cast<const uint4*>(vrow + at), v1 = *reinterpret_cast<const uint4*>(vrow + T::kRowV + at);
+            const uint4 v2 = *reinterpret_cast<const uint4*>(vrow + 8 * T::kRowV + at);
+            const uint4 v3 = *reinterpret_cast<const uint4*>(vrow + 9 * T::kRowV + at);
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+            const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(o[4 * i + e][nt], __byte_perm(w0[e], w1[e], 0x5410), __byte_perm(w0[e], w1[e], 0x7632),
-                       __byte_perm(w2[e], w3[e], 0x5410), __byte_perm(w2[e], w3[e], 0x7632), pb[nt][0], pb[nt][1]);
+            for (int e = 0; e < 4; ++e)   // word e holds dims 2 e and 2 e + 1 of the lane's eight
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_bf16(o[4 * i + e][nt], __byte_perm(w0[e], w1[e], 0x5410), __byte_perm(w0[e], w1[e], 0x7632),
+                         __byte_perm(w2[e], w3[e], 0x5410), __byte_perm(w2[e], w3[e], 0x7632), pb[nt][0], pb[nt][1]);
+          }
         }
       }
     }
@@ -838,35 +930,37 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
   if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
-// Warps per block, blocks per SM and stages of the ring.  Sixteen rows need about 170 registers a
-// thread, eight about 128.
+// Warps per block, blocks per SM, tiles of 16 tokens per step and stages of the ring.
 template <bool INT4, int NT>
 struct Shape {
-  static constexpr int W = INT4 ? (NT == 2 ? 8 : 4) : 8;
-  static constexpr int B = INT4 ? (NT == 2 ? 1 : 3) : 1;
-  static constexpr int S = INT4 ? (NT == 2 ? 6 : 4) : 2;
+  static constexpr int W = INT4 ? 4 : 8;
+  static constexpr int B = INT4 ? (NT == 2 ? 2 : 4) : 1;
+  static constexpr int U = INT4 ? 2 : 1, S = INT4 && NT == 2 ? 3 : 2;
 };
-int warps_of(bool int4, bool nt2) { return int4 ? (nt2 ? Shape<true, 2>::W : Shape<true, 1>::W) : Shape<false, 1>::W; }
-int blocks_of(bool int4, bool nt2) { return int4 ? (nt2 ? Shape<true, 2>::B : Shape<true, 1>::B) : Shape<false, 1>::B; }
+template <class F>
+auto with_shape(bool int4, bool nt2, F f) {
+  return int4 ? (nt2 ? f(Shape<true, 2>()) : f(Shape<true, 1>())) : nt2 ? f(Shape<false, 2>()) : f(Shape<false, 1>());
+}
 
 constexpr int kSms = 148;
-constexpr int kWholeTiles = 32;   // items of at most 512 tokens are not cut
+constexpr int kWholeTokens = 512;   // items up to this length are not cut
 
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   Plan p;
   const int R = a.n_new * a.G;
   p.nt2 = R > 8;
-  const int W = warps_of(c.int4, p.nt2);
+  int W = 0, step = 0, resident = 0;
+  with_shape(c.int4, p.nt2, [&](auto h) { W = h.W; step = kTile * h.U; resident = h.B; });
   p.row_groups = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   p.tile_rows = (p.nt2 ? 16 : 8) * p.row_groups;
   p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
   // the most tiles an item can have
   long long range = a.max_seqlen;
   if (a.window > 0) range = std::min<long long>(range, (long long)a.window + a.n_new + kTile);
-  const long long tiles = (range + kTile - 1) / kTile, items = (long long)c.batch * c.h_kv * p.row_tiles;
+  const long long tiles = (range + step - 1) / step, items = (long long)c.batch * c.h_kv * p.row_tiles;
   p.min_tiles = 2 * (W / p.row_groups);
-  p.whole = tiles <= kWholeTiles;
-  const long long most = (long long)kSms * blocks_of(c.int4, p.nt2);
+  p.whole = range <= kWholeTokens;
+  const long long most = (long long)kSms * resident;
   // items <= 2^31 (cache_attn_fits), tiles <= 2^26
   p.blocks = (int)(p.whole ? std::min<long long>(items, INT32_MAX) : std::min(most, (items * tiles + p.min_tiles - 1) / p.min_tiles));
   return p;
@@ -888,18 +982,19 @@ Parts parts_of(const CacheArgs& c, const Plan& p) {
 template <bool INT4, int DK, int DV, int NT, bool EXT>
 cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, cudaStream_t st) {
   using H = Shape<INT4, NT>;
-  constexpr int kSmem = attn_smem<INT4, DK, DV, NT, H::W, H::S>();
-  static_assert(kSmem * H::B <= 227 * 1024, "the rings of the resident blocks fit an SM");
+  constexpr int kRing = H::W * warp_smem<INT4, DK, DV, NT, H::U, H::S>(), kQ = query_smem<INT4, DK, NT>();
+  static_assert((kRing + kQ + 2048) * H::B <= 228 * 1024, "the rings of the resident blocks fit an SM");
+  static_assert(kRing + 4 * kQ <= 227 * 1024, "a block's shared memory");
   static PerDevice set;
-  auto* f = cache_attn_kernel<INT4, DK, DV, NT, H::W, H::B, H::S, EXT>;
-  cudaError_t e = set.once([&] { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+  auto* f = cache_attn_kernel<INT4, DK, DV, NT, H::W, H::B, H::U, H::S, EXT>;
+  cudaError_t e = set.once([&] { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 4 * kQ); });
   if (e != cudaSuccess) return e;
   const Parts x = parts_of(c, p);
   char* ws = static_cast<char*>(a.workspace);
   Cut* cuts = reinterpret_cast<Cut*>(ws);
   float2* ml = reinterpret_cast<float2*>(ws + x.ml);
   float* o = reinterpret_cast<float*>(ws + x.o);
-  f<<<p.blocks, H::W * 32, kSmem, st>>>(c, a, p, cuts, ml, o);
+  f<<<p.blocks, H::W * 32, kRing + p.row_groups * kQ, st>>>(c, a, p, cuts, ml, o);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
   // few items, many parts each: a block per row; else a warp per row
