@@ -89,6 +89,11 @@ def compress_torch(x, w, l=32, s=16):
     return out
 
 
+# the current stream's handle, without the Stream object around it where torch offers that
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -142,14 +147,15 @@ class KVCache:
         self.k, self.v, self.k_scale, self.v_scale = pools
         self.page_table = table
         self.device = self.k.device
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         for t in (self.k, self.v, self.page_table):
             _need(t.is_cuda and t.device == self.device and t.is_contiguous(), "pools and page table: contiguous, on one GPU")
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         p = lambda t: t.data_ptr() if t is not None else None
         self.desc = NsaCache(format=NSA_CACHE_INT4 if fmt == "int4" else NSA_CACHE_BF16, batch=batch, h_kv=h_kv, d_k=d_k,
                              d_v=d_v, page_size=page_size, n_pages=self.k.shape[0], max_pages=table.shape[1],
                              k=p(self.k), v=p(self.v), k_scale=p(self.k_scale), v_scale=p(self.v_scale),
                              page_table=p(table), status=p(self.status))
+        self._workspaces = {}   # bytes by (n, h_q, max_seqlen, window)
 
     @property
     def max_len(self):
@@ -159,29 +165,57 @@ class KVCache:
         """The status word after a synchronised call: 0, or NSA_CODE_CACHE."""
         return int(self.status.item())
 
-    def _lengths(self, seqlens, cu_seqlens):
-        for t, n, name in ((seqlens, self.batch, "seqlens"), (cu_seqlens, self.batch + 1, "cu_seqlens")):
-            if t is not None:
-                _need(t.dtype == torch.int32 and t.shape == (n,) and t.device == self.device and t.is_contiguous(),
-                      f"{name}: int32 [{n}] on {self.device}")
+    # A single token's calls take as long on the host as on the GPU: checks are plain conditions, and
+    # their messages are made only when one fails.
+
+    def _call(self, fn, stream, *args):
+        """fn(cache, ..., stream) with the cache's device current; raises NsaError for a refusal."""
+        index = self.device.index
+        if stream is None:
+            stream = _current_stream(index)
+        if torch.cuda.current_device() == index:
+            return fn(self.desc, *args, stream=stream)
+        with torch.cuda.device(index):
+            return fn(self.desc, *args, stream=stream)
+
+    def _lengths(self, t, n, name):
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous int32 [{n}] on {self.device}")
+        return t.data_ptr()
 
     def _rows(self, x, heads, d, packed, name):
         """Checks new rows [batch, n, heads, d] (packed: [total, heads, d]); the elements from one
         token to the next.  Tokens may lie apart (a slice of a wider row), a token's heads not."""
-        lead = 1 if packed else 2
-        _need(x.dim() == lead + 2 and x.shape[-2:] == (heads, d) and (packed or x.shape[0] == self.batch),
-              f"{name}: {'[total' if packed else f'[{self.batch}, n'}, {heads}, {d}], not {tuple(x.shape)}")
-        _need(x.dtype == torch.bfloat16 and x.device == self.device, f"{name}: bf16 on {self.device}")
-        _need(x.stride(-1) == 1 and (heads == 1 or x.stride(-2) == d), f"{name}: heads and dims must be contiguous")
-        if x.shape[:-2].numel() <= 1:
+        shape = x.shape
+        if len(shape) != (3 if packed else 4) or shape[-2] != heads or shape[-1] != d or not (packed or shape[0] == self.batch):
+            raise ValueError(f"{name}: {'[total' if packed else f'[{self.batch}, n'}, {heads}, {d}], not {tuple(shape)}")
+        if x.dtype is not torch.bfloat16 or x.device != self.device:
+            raise ValueError(f"{name}: bf16 on {self.device}")
+        stride = x.stride()
+        if stride[-1] != 1 or (heads > 1 and stride[-2] != d):
+            raise ValueError(f"{name}: heads and dims must be contiguous")
+        tokens = shape[0] if packed else shape[0] * shape[1]
+        if tokens <= 1:
             return max(heads * d, 8)
-        step, n = x.stride(-3), x.shape[-3]
-        if not packed and x.shape[0] > 1:
-            if n == 1:
-                step = x.stride(0)
-            else:
-                _need(x.stride(0) == n * step, f"{name}: tokens must lie at one stride")
-        return step
+        if packed or shape[0] == 1:
+            return stride[-3]
+        if shape[1] == 1:
+            return stride[0]
+        if stride[0] != shape[1] * stride[1]:
+            raise ValueError(f"{name}: tokens must lie at one stride")
+        return stride[1]
+
+    def _like(self, t, shape, dtype, name):
+        """Checks a given output or table."""
+        if tuple(t.shape) != tuple(shape) or t.dtype is not dtype or t.device != self.device or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def _new(self, shape, dtype, stream):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if stream is not None:   # torch must not hand the memory out again before that stream is done
+            t.record_stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
+        return t
 
     def append(self, k, v, seqlens, *, cu_seqlens=None, cos_sin=None, interleaved=False, q=None, q_out=None, stream=None):
         """Write new tokens: k [batch, n, h_kv, d_k] and v [batch, n, h_kv, d_v] are the last n of
@@ -189,53 +223,54 @@ class KVCache:
         cos_sin fp32 [positions, rot_dim] (cosines, then sines) rotates the keys by their
         positions, and the queries q [.., h_q, d_k], which are returned (into q_out)."""
         packed = cu_seqlens is not None
-        self._lengths(seqlens, cu_seqlens)
-        a = NsaCacheAppendArgs(seqlens=seqlens.data_ptr(), k=k.data_ptr(), v=v.data_ptr())
-        a.k_stride = self._rows(k, self.h_kv, self.d_k, packed, "k")
-        a.v_stride = self._rows(v, self.h_kv, self.d_v, packed, "v")
-        _need(k.shape[:-2] == v.shape[:-2], "k and v must hold the same tokens")
+        k_stride, v_stride = self._rows(k, self.h_kv, self.d_k, packed, "k"), self._rows(v, self.h_kv, self.d_v, packed, "v")
+        lead = k.shape[:-2]
+        if v.shape[:-2] != lead:
+            raise ValueError("k and v must hold the same tokens")
+        a = NsaCacheAppendArgs(k.data_ptr(), v.data_ptr(), None, None, self._lengths(seqlens, self.batch, "seqlens"))
+        a.k_stride, a.v_stride = k_stride, v_stride
         if packed:
-            a.cu_seqlens, a.total_tokens = cu_seqlens.data_ptr(), k.shape[0]
+            a.cu_seqlens, a.total_tokens = self._lengths(cu_seqlens, self.batch + 1, "cu_seqlens"), lead[0]
         else:
-            a.n_new = k.shape[1]
+            a.n_new = lead[1]
         if cos_sin is not None:
-            _need(cos_sin.dim() == 2 and cos_sin.dtype == torch.float32 and cos_sin.device == self.device and
-                  cos_sin.is_contiguous(), f"cos_sin: contiguous fp32 [positions, rot_dim] on {self.device}")
-            a.cos_sin, a.n_positions, a.rot_dim = cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
-            a.interleaved = int(interleaved)
+            if cos_sin.dim() != 2:
+                raise ValueError("cos_sin: [positions, rot_dim]")
+            a.n_positions, a.rot_dim = cos_sin.shape
+            a.cos_sin, a.interleaved = self._like(cos_sin, cos_sin.shape, torch.float32, "cos_sin"), int(interleaved)
         if q is not None:
-            a.q_stride = self._rows(q, q.shape[-2], self.d_k, packed, "q")
-            _need(q.shape[:-2] == k.shape[:-2], "q must hold the same tokens as k")
+            if q.dim() < 2:
+                raise ValueError("q: the new tokens' queries, [.., h_q, d_k]")
+            h_q = q.shape[-2]
+            a.q_stride = self._rows(q, h_q, self.d_k, packed, "q")
+            if q.shape[:-2] != lead:
+                raise ValueError("q must hold the same tokens as k")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.device == q.device and
-                  q_out.is_contiguous(), "q_out: contiguous, like q")
-            a.q, a.q_out, a.h_q = q.data_ptr(), q_out.data_ptr(), q.shape[-2]
-        if k.shape[:-2].numel():   # no tokens: nothing to do
-            with torch.cuda.device(self.device):
-                nsa_cache_append(self.desc, a, torch.cuda.current_stream() if stream is None else stream)
+                q_out = self._new(q.shape, torch.bfloat16, stream)
+            a.q, a.q_out, a.h_q = q.data_ptr(), self._like(q_out, q.shape, torch.bfloat16, "q_out"), h_q
+        if lead.numel():   # no tokens: nothing to do
+            self._call(nsa_cache_append, stream, a)
         return q_out if q is not None else None
 
     def read(self, seqlens, n=None, *, cu_seqlens=None, total=None, k_out=None, v_out=None, stream=None):
         """The last n tokens of each sequence as contiguous bf16 (k [batch, n, h_kv, d_k], v), or,
         with cu_seqlens, the last cu[b+1] - cu[b] of each, packed into ``total`` rows."""
         packed = cu_seqlens is not None
-        self._lengths(seqlens, cu_seqlens)
-        _need(total is not None if packed else n is not None, "read takes n, or cu_seqlens and total")
+        self._lengths(seqlens, self.batch, "seqlens")
+        if packed:
+            self._lengths(cu_seqlens, self.batch + 1, "cu_seqlens")
+        if (total if packed else n) is None:
+            raise ValueError("read takes n, or cu_seqlens and total")
         lead = (int(total),) if packed else (self.batch, int(n))
-        _need(min(lead) >= 0, "read takes a number of tokens")
-        outs = []
-        for t, d, name in ((k_out, self.d_k, "k_out"), (v_out, self.d_v, "v_out")):
-            if t is None:
-                t = torch.empty((*lead, self.h_kv, d), dtype=torch.bfloat16, device=self.device)
-            _need(t.shape == (*lead, self.h_kv, d) and t.dtype == torch.bfloat16 and t.device == self.device and
-                  t.is_contiguous(), f"{name}: contiguous bf16 {(*lead, self.h_kv, d)} on {self.device}")
-            outs.append(t)
-        if outs[0].numel():
-            with torch.cuda.device(self.device):
-                nsa_cache_read(self.desc, seqlens, cu_seqlens, 0 if packed else lead[1], lead[0] if packed else 0, *outs,
-                               stream=torch.cuda.current_stream() if stream is None else stream)
-        return tuple(outs)
+        if lead[-1] < 0:
+            raise ValueError("read takes a number of tokens")
+        shapes = (*lead, self.h_kv, self.d_k), (*lead, self.h_kv, self.d_v)
+        k_out = self._new(shapes[0], torch.bfloat16, stream) if k_out is None else k_out
+        v_out = self._new(shapes[1], torch.bfloat16, stream) if v_out is None else v_out
+        k_ptr, v_ptr = self._like(k_out, shapes[0], torch.bfloat16, "k_out"), self._like(v_out, shapes[1], torch.bfloat16, "v_out")
+        if lead[-1]:
+            self._call(nsa_cache_read, stream, seqlens, cu_seqlens, 0 if packed else lead[1], lead[0] if packed else 0, k_ptr, v_ptr)
+        return k_out, v_out
 
     def attend(self, q, seqlens, max_seqlen=None, *, softmax_scale=0.0, softcap=0.0, slopes=None, window=0, out=None,
                lse=None, workspace=None, stream=None):
@@ -245,35 +280,30 @@ class KVCache:
         (fp32 [h_q]) adds slope * (u - p), window (0: none) keeps the last tokens; lse (fp32
         [batch, n, h_q]) receives the log-sum-exps.  The workspace is torch's unless one of
         attend_workspace() bytes is given."""
-        self._lengths(seqlens, None)
-        _need(q.dim() == 4 and q.shape[0] == self.batch and q.shape[1] >= 1 and q.shape[3] == self.d_k and
-              q.dtype == torch.bfloat16 and q.device == self.device and q.is_contiguous(),
-              f"q: contiguous bf16 [{self.batch}, n, h_q, {self.d_k}] on {self.device}")
+        if q.dim() != 4 or q.shape[0] != self.batch or q.shape[1] < 1 or q.shape[3] != self.d_k or \
+                q.dtype is not torch.bfloat16 or q.device != self.device or not q.is_contiguous():
+            raise ValueError(f"q: contiguous bf16 [{self.batch}, n, h_q, {self.d_k}] on {self.device}")
         B, n, h_q, _ = q.shape
         if out is None:
-            out = torch.empty((B, n, h_q, self.d_v), dtype=torch.bfloat16, device=self.device)
-        _need(out.shape == (B, n, h_q, self.d_v) and out.dtype == torch.bfloat16 and out.device == self.device and
-              out.is_contiguous(), "out: contiguous bf16 [batch, n, h_q, d_v]")
-        for t, shape, name in ((slopes, (h_q,), "slopes"), (lse, (B, n, h_q), "lse")):
-            _need(t is None or (t.shape == shape and t.dtype == torch.float32 and t.device == self.device and
-                                t.is_contiguous()), f"{name}: contiguous fp32 {shape} on {self.device}")
-        a = NsaCacheAttentionArgs(seqlens=seqlens.data_ptr(), softmax_scale=softmax_scale, softcap=softcap, n_new=n,
-                                  h_q=h_q, max_seqlen=self.max_len if max_seqlen is None else max_seqlen, window=window)
-        if slopes is not None:
-            a.slopes = slopes.data_ptr()
-        if lse is not None:
-            a.lse = lse.data_ptr()
+            out = self._new((B, n, h_q, self.d_v), torch.bfloat16, stream)
+        out_ptr = self._like(out, (B, n, h_q, self.d_v), torch.bfloat16, "out")
+        max_seqlen = self.max_len if max_seqlen is None else max_seqlen
+        a = NsaCacheAttentionArgs(self._lengths(seqlens, self.batch, "seqlens"),
+                                  None if slopes is None else self._like(slopes, (h_q,), torch.float32, "slopes"),
+                                  None if lse is None else self._like(lse, (B, n, h_q), torch.float32, "lse"),
+                                  None, 0, softmax_scale, softcap, n, h_q, max_seqlen, window)
         if workspace is None:
-            need = nsa_cache_attention_workspace(self.desc, a)
+            key = (n, h_q, max_seqlen, window)
+            need = self._workspaces.get(key)
+            if need is None:
+                if len(self._workspaces) >= 64:
+                    self._workspaces.clear()
+                need = self._workspaces[key] = nsa_cache_attention_workspace(self.desc, a)
             if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-                if stream is not None:   # torch must not hand it out again before that stream is done
-                    workspace.record_stream(torch.cuda.ExternalStream(stream, device=self.device)
-                                            if isinstance(stream, int) else stream)
+                workspace = self._new((need,), torch.uint8, stream)
         if workspace is not None:
             a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        with torch.cuda.device(self.device):
-            nsa_cache_attention(self.desc, q, a, out, torch.cuda.current_stream() if stream is None else stream)
+        self._call(nsa_cache_attention, stream, q.data_ptr(), a, out_ptr)
         return out
 
     def attend_workspace(self, n, h_q, max_seqlen=None, window=0):
