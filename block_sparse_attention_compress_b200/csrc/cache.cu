@@ -63,25 +63,31 @@ __device__ __forceinline__ uint4 rotated_chunk(const __nv_bfloat16* head, int d0
   return pack8(y);
 }
 
-// Codes of 8 consecutive values of a row (one 32-bit word, low nibble first) and the group's
-// (s, z).  The four lanes of a quad hold the four chunks of one group of 32.
-__device__ __forceinline__ uint32_t quantise_chunk(const uint4& u, uint32_t& sz) {
-  float x[8];
-  unpack8(u, x);
-  float lo = x[0], hi = x[0], odd = 0.f;   // odd: NaN as soon as one value is not finite
+// Least and largest of 8 values, and NaN as soon as one of them is not finite.
+struct Range {
+  float lo, hi, odd;
+};
+__device__ __forceinline__ Range range_of(const float (&x)[8]) {
+  Range r{x[0], x[0], 0.f};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    odd = __fmaf_rn(x[i], 0.f, odd);
+    r.lo = fminf(r.lo, x[i]);
+    r.hi = fmaxf(r.hi, x[i]);
+    r.odd = __fmaf_rn(x[i], 0.f, r.odd);
   }
-  const uint32_t quad = 0xfu << (threadIdx.x & 28);
-#pragma unroll
-  for (int o = 1; o <= 2; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(quad, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(quad, hi, o));
-    odd += __shfl_xor_sync(quad, odd, o);
-  }
+  return r;
+}
+__device__ __forceinline__ Range both(const Range& a, const Range& b) {
+  return Range{fminf(a.lo, b.lo), fmaxf(a.hi, b.hi), a.odd + b.odd};
+}
+__device__ __forceinline__ Range across(const Range& r, int lanes, uint32_t mask) {
+  return both(r, Range{__shfl_xor_sync(mask, r.lo, lanes), __shfl_xor_sync(mask, r.hi, lanes), __shfl_xor_sync(mask, r.odd, lanes)});
+}
+
+// Codes of 8 consecutive values of a row (one 32-bit word, low nibble first) and the (s, z) of their
+// group, whose range is r.
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[8], const Range& r, uint32_t& sz) {
+  const float lo = r.lo, hi = r.hi, odd = r.odd;
   const float span = __fsub_rn(hi, lo);
   if (!(span < INFINITY) || odd != 0.f || isnan(odd)) {
     sz = 0x7fc07fc0u;
@@ -95,11 +101,19 @@ __device__ __forceinline__ uint32_t quantise_chunk(const uint4& u, uint32_t& sz)
   uint32_t w = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float c = fminf(fmaxf(__fadd_rn(rintf(__fmul_rn(__fsub_rn(x[i], z), inv)), 8.f), 0.f), 15.f);
-    w |= (uint32_t)(int)c << (4 * i);
+    // in [-8, 7] and on top of 1.5 * 2^23 the sum's rounding (nearest, even) is the integer's
+    const float c = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], z), inv), -8.f), 7.f);
+    w |= (__float_as_uint(__fadd_rn(c, 12582920.f)) & 15u) << (4 * i);
   }
   sz = pack_bf16(s, z);
   return w;
+}
+// The same where the four lanes of a quad hold the four chunks of one group of 32.
+__device__ __forceinline__ uint32_t quantise_chunk(const uint4& u, uint32_t& sz) {
+  float x[8];
+  unpack8(u, x);
+  const uint32_t quad = 0xfu << (threadIdx.x & 28);
+  return codes_of(x, across(across(range_of(x), 1, quad), 2, quad), sz);
 }
 
 // Stores the word of values 8 n .. 8 n + 7 of a row of DIM values at its place in the stored order.
@@ -128,16 +142,19 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* row, int n) {
 }
 
 // One chunk (8 values) of a new key or value row into the cache.
+template <int DIM, bool KEY>
+__device__ __forceinline__ void put_codes(const CacheArgs& c, const Row& w, int h, int n, uint32_t codes, uint32_t sz) {
+  const size_t row = ((size_t)w.page * c.h_kv + h) * c.page_size + w.place;
+  store_codes<DIM, KEY>(static_cast<uint8_t*>(KEY ? c.k : c.v) + row * (DIM / 2), n, codes);
+  if ((n & 3) == 0) reinterpret_cast<uint32_t*>(KEY ? c.k_scale : c.v_scale)[row * (DIM / 32) + (n >> 2)] = sz;
+}
 template <int DIM, bool KEY, bool INT4>
 __device__ __forceinline__ void put_chunk(const CacheArgs& c, const Row& w, int h, int n, const uint4& u) {
   void* pool = KEY ? c.k : c.v;
   if constexpr (INT4) {
     uint32_t sz;
     const uint32_t codes = quantise_chunk(u, sz);
-    const size_t row = ((size_t)w.page * c.h_kv + h) * c.page_size + w.place;
-    store_codes<DIM, KEY>(static_cast<uint8_t*>(pool) + row * (DIM / 2), n, codes);
-    if ((n & 3) == 0)
-      reinterpret_cast<uint32_t*>(KEY ? c.k_scale : c.v_scale)[row * (DIM / 32) + (n >> 2)] = sz;
+    put_codes<DIM, KEY>(c, w, h, n, codes, sz);
   } else {
     const size_t row = ((size_t)w.page * c.page_size + w.place) * c.h_kv + h;
     reinterpret_cast<uint4*>(pool)[row * (DIM / 8) + n] = u;
@@ -145,9 +162,26 @@ __device__ __forceinline__ void put_chunk(const CacheArgs& c, const Row& w, int 
 }
 
 // A block's tokens, looked up by its first threads.
-constexpr int kThreads = 256, kMaxTokens = 8, kFlight = 4;   // kFlight: rows of a thread in flight
+// kFlight: heads (kReadFlight: units of 16 values) a thread has in flight.  Append with 2 at 4 blocks an SM
+// moves 64K tokens of (64, 4) heads in 622 us (3.44 GB, 5.5 TB/s), with 2 at 3 blocks in 735, with 4 at 2
+// blocks in 749, with 1 at 4 in 722; read with 2 gives back 128K tokens of 4 heads in 90 us, with 4 in 109.
+constexpr int kThreads = 256, kMaxTokens = 8, kFlight = 2, kReadFlight = 2;
 struct Place : Row {
   bool live;   // written (append) or there (read)
+};
+
+// The chunks (of 8 or 16 values) of a block's tokens, `per` each, end to end: a thread's own ones, kThreads apart.
+struct Chunks {
+  int tok, y, dtok, dy;
+  __device__ __forceinline__ Chunks(int tid, int per) : tok(tid / per), y(tid % per), dtok(kThreads / per), dy(kThreads % per) {}
+  __device__ __forceinline__ void next(int per) {
+    tok += dtok;
+    y += dy;
+    if (y >= per) {
+      y -= per;
+      ++tok;
+    }
+  }
 };
 
 // Sixteen values of a head, in two chunks of 8: the pairs of angles 8 u .. 8 u + 7.
@@ -176,7 +210,7 @@ __device__ __forceinline__ void turn(uint4& lo, uint4& hi, const Angles& t, bool
 }
 
 template <int DK, int DV, bool INT4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const CacheArgs c, const RowsArgs r, const AppendArgs a, int tokens) {
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheArgs c, const RowsArgs r, const AppendArgs a, int tokens) {
   __shared__ Place s_place[kMaxTokens];
   const int i0 = blockIdx.x * tokens, n = min(tokens, r.rows - i0), tid = threadIdx.x;
   if (tid < n) {
@@ -188,14 +222,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheArgs c, con
   }
   __syncthreads();
 
-  // queries, and keys of a bf16 cache: sixteen values a thread, the same ones of every head, so that a
-  // thread loads its angles once a token
+  // queries and keys: sixteen values a thread, the same ones of every head, so that a thread loads its
+  // angles once a token.  4 bits: the chunks of a group of 32 are then those of a quad of threads (pairs (j, j + rot / 2),
+  // rot a multiple of 64) or both chunks of two threads (interleaved pairs); other rotations take the
+  // keys chunk by chunk below.
   constexpr int kUnits = DK / 16, kSlots = kThreads / kUnits;
   const int u = tid % kUnits, slot = tid / kUnits;
-  const int nq = a.q ? a.h_q : 0, heads = nq + (INT4 ? 0 : c.h_kv);
-  const bool turned = a.cos_sin != nullptr && u < a.rot / 16;
+  const int rot = a.cos_sin ? a.rot : 0, nq = a.q ? a.h_q : 0;
+  const bool by_chunk = INT4 && !a.interleaved && rot % 64;
+  const int heads = nq + (by_chunk ? 0 : c.h_kv);
+  const bool turned = u < rot / 16;
   // chunks (of 8 values) of the unit
-  const int c0 = turned && !a.interleaved ? u : 2 * u, c1 = turned && !a.interleaved ? u + a.rot / 16 : 2 * u + 1;
+  const int c0 = a.interleaved ? 2 * u : turned ? u : rot / 16 + u;
+  const int c1 = a.interleaved ? 2 * u + 1 : turned ? u + rot / 16 : u + DK / 16;
   for (int x = 0; x < n && slot < kSlots; ++x) {
     const Place p = s_place[x];
     if (p.seq < 0) continue;
@@ -229,6 +268,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheArgs c, con
         const int h = h0 + f * kSlots;
         if (h >= end) break;
         if (turned && p.live) turn(lo[f], hi[f], t, a.interleaved);
+        if (INT4 && h >= nq) {
+          float x[2][8];
+          unpack8(lo[f], x[0]);
+          unpack8(hi[f], x[1]);
+          Range g[2] = {range_of(x[0]), range_of(x[1])};
+          const uint32_t quad = 0xfu << (tid & 28);   // all of a head
+          if (a.interleaved) {
+            g[0] = g[1] = across(both(g[0], g[1]), 1, quad);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) g[e] = across(across(g[e], 1, quad), 2, quad);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t sz;
+            const uint32_t codes = codes_of(x[e], g[e], sz);
+            put_codes<DK, true>(c, p, h - nq, e ? c1 : c0, codes, sz);
+          }
+          continue;
+        }
         uint4* dst = h < nq ? qo + h * (DK / 8) : ko + (h - nq) * (DK / 8);
         dst[c0] = lo[f];
         dst[c1] = hi[f];
@@ -236,57 +295,72 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const CacheArgs c, con
     }
   }
 
-  // keys of a 4-bit cache and values: a chunk of 8 values a thread, the tokens' chunks end to end
-  const int nk = INT4 ? c.h_kv * (DK / 8) : 0, nv = c.h_kv * (DV / 8), per = nk + nv;
+  // values (and keys by chunks): a chunk of 8 values a thread, the tokens' chunks end to end
+  const int nk = by_chunk ? c.h_kv * (DK / 8) : 0, nv = c.h_kv * (DV / 8), per = nk + nv;
+  Chunks at(tid, per);
   for (int x0 = tid; x0 < n * per; x0 += kFlight * kThreads) {
     uint4 v[kFlight];
+    int tok[kFlight], y[kFlight];
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int x = x0 + f * kThreads, tok = x / per, y = x - tok * per;
-      if (x >= n * per) break;
-      const Place& p = s_place[tok];
-      if (!p.live) continue;
-      const size_t i = (size_t)i0 + tok;
-      if (INT4 && y < nk)
-        v[f] = rotated_chunk(static_cast<const __nv_bfloat16*>(a.k) + i * a.k_stride + y / (DK / 8) * DK, y % (DK / 8) * 8,
-                             a.cos_sin ? a.cos_sin + (size_t)p.pos * a.rot : nullptr, a.rot, a.interleaved);
+      tok[f] = at.tok;
+      y[f] = at.y;
+      at.next(per);
+      if (tok[f] >= n || !s_place[tok[f]].live) continue;
+      const size_t i = (size_t)i0 + tok[f];
+      if (INT4 && y[f] < nk)
+        v[f] = rotated_chunk(static_cast<const __nv_bfloat16*>(a.k) + i * a.k_stride + y[f] / (DK / 8) * DK, y[f] % (DK / 8) * 8,
+                             a.cos_sin ? a.cos_sin + (size_t)s_place[tok[f]].pos * a.rot : nullptr, a.rot, a.interleaved);
       else
-        v[f] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + i * a.v_stride) + (y - nk));
+        v[f] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + i * a.v_stride) + (y[f] - nk));
     }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int x = x0 + f * kThreads, tok = x / per, y = x - tok * per;
-      if (x >= n * per) break;
-      const Place& p = s_place[tok];
-      if (!p.live) continue;   // per is a multiple of 4: a quad's threads stay together
-      if (INT4 && y < nk) put_chunk<DK, true, INT4>(c, p, y / (DK / 8), y % (DK / 8), v[f]);
-      else put_chunk<DV, false, INT4>(c, p, (y - nk) / (DV / 8), (y - nk) % (DV / 8), v[f]);
+      if (tok[f] >= n || !s_place[tok[f]].live) continue;   // per is a multiple of 4: a quad's threads stay together
+      const int z = y[f] - nk;
+      if (INT4 && z < 0) put_chunk<DK, true, INT4>(c, s_place[tok[f]], y[f] / (DK / 8), y[f] % (DK / 8), v[f]);
+      else put_chunk<DV, false, INT4>(c, s_place[tok[f]], z / (DV / 8), z % (DV / 8), v[f]);
     }
   }
 }
 
-// What a chunk of 8 values is made from: the row itself (bf16), or the codes' word and the group's (s, z).
+// Sixteen values (unit u of a row): the row itself (bf16), or their two words of codes and the group's (s, z).
+struct Sixteen {
+  uint4 a, b;
+};
 template <int DIM, bool KEY, bool INT4>
-__device__ __forceinline__ uint4 fetch_chunk(const CacheArgs& c, const Row& w, int h, int n) {
+__device__ __forceinline__ Sixteen fetch(const CacheArgs& c, const Row& w, int h, int u) {
   const void* pool = KEY ? c.k : c.v;
+  Sixteen r;
   if constexpr (!INT4) {
     const size_t row = ((size_t)w.page * c.page_size + w.place) * c.h_kv + h;
-    return __ldg(reinterpret_cast<const uint4*>(pool) + row * (DIM / 8) + n);
+    const uint4* src = reinterpret_cast<const uint4*>(pool) + row * (DIM / 8) + 2 * u;
+    r.a = __ldg(src);
+    r.b = __ldg(src + 1);
   } else {
     const size_t row = ((size_t)w.page * c.h_kv + h) * c.page_size + w.place;
-    const uint32_t codes = load_codes<DIM, KEY>(static_cast<const uint8_t*>(pool) + row * (DIM / 2), n);
-    const uint32_t* sz = reinterpret_cast<const uint32_t*>(KEY ? c.k_scale : c.v_scale) + row * (DIM / 32) + (n >> 2);
-    return make_uint4(codes, __ldg(sz), 0, 0);
+    const uint8_t* src = static_cast<const uint8_t*>(pool) + row * (DIM / 2);
+    r.a.x = load_codes<DIM, KEY>(src, 2 * u);
+    r.a.y = load_codes<DIM, KEY>(src, 2 * u + 1);
+    r.a.z = __ldg(reinterpret_cast<const uint32_t*>(KEY ? c.k_scale : c.v_scale) + row * (DIM / 32) + (u >> 1));
   }
+  return r;
 }
-template <bool INT4>
-__device__ __forceinline__ uint4 chunk_value(const uint4& u) {
-  if constexpr (!INT4) return u;
-  const float s = cache::bf16_lo(u.y), z = cache::bf16_hi(u.y);
-  float x[8];
+// The values of a word of codes.  128 + c is a bf16 with c as its last bits; less 136, times s, plus z in one
+// fma: the value rounded once.
+__device__ __forceinline__ uint4 values_of(uint32_t w, uint32_t sz) {
+  const __nv_bfloat162 pair = *reinterpret_cast<const __nv_bfloat162*>(&sz);
+  const __nv_bfloat162 s = __low2bfloat162(pair), z = __high2bfloat162(pair);
+  uint32_t v[4];   // values j and j + 4
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = __fmaf_rn(s, (float)((int)(u.x >> (4 * j) & 15u) - 8), z);   // s (c - 8) is exact
-  return pack8(x);
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = ((w >> (4 * j)) & 0x000f000fu) | 0x43004300u, o = 0x43084308u;
+    const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&o));
+    const __nv_bfloat162 y = __hfma2(s, c, z);
+    v[j] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                    __byte_perm(v[2], v[3], 0x7632));
 }
 
 template <int DK, int DV, bool INT4>
@@ -302,28 +376,30 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheArgs c, const
     s_place[tid] = p;
   }
   __syncthreads();
-  const int nk = c.h_kv * (DK / 8), nv = c.h_kv * (DV / 8), per = nk + nv;
-  for (int x0 = tid; x0 < n * per; x0 += kFlight * kThreads) {
-    uint4 u[kFlight];
+  const int nk = c.h_kv * (DK / 16), nv = c.h_kv * (DV / 16), per = nk + nv;
+  Chunks at(tid, per);
+  for (int x0 = tid; x0 < n * per; x0 += kReadFlight * kThreads) {
+    Sixteen v[kReadFlight];
+    int tok[kReadFlight], y[kReadFlight];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int x = x0 + f * kThreads, tok = x / per, y = x - tok * per;
-      if (x >= n * per) break;
-      const Place& p = s_place[tok];
-      if (!p.live) continue;
-      u[f] = y < nk ? fetch_chunk<DK, true, INT4>(c, p, y / (DK / 8), y % (DK / 8))
-                    : fetch_chunk<DV, false, INT4>(c, p, (y - nk) / (DV / 8), (y - nk) % (DV / 8));
+    for (int f = 0; f < kReadFlight; ++f) {
+      tok[f] = at.tok;
+      y[f] = at.y;
+      at.next(per);
+      if (tok[f] >= n || !s_place[tok[f]].live) continue;
+      const int z = y[f] - nk;
+      v[f] = z < 0 ? fetch<DK, true, INT4>(c, s_place[tok[f]], y[f] / (DK / 16), y[f] % (DK / 16))
+                   : fetch<DV, false, INT4>(c, s_place[tok[f]], z / (DV / 16), z % (DV / 16));
     }
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int x = x0 + f * kThreads, tok = x / per, y = x - tok * per;
-      if (x >= n * per) break;
-      const Place& p = s_place[tok];
-      if (p.seq < 0) continue;
-      const size_t i = (size_t)i0 + tok;
-      const uint4 o = p.live ? chunk_value<INT4>(u[f]) : make_uint4(0, 0, 0, 0);
-      if (y < nk) k_out[i * nk + y] = o;
-      else v_out[i * nv + y - nk] = o;
+    for (int f = 0; f < kReadFlight; ++f) {
+      if (tok[f] >= n || s_place[tok[f]].seq < 0) continue;
+      const size_t i = (size_t)i0 + tok[f];
+      uint4* dst = 2 * (y[f] < nk ? i * nk + y[f] : i * nv + y[f] - nk) + (y[f] < nk ? k_out : v_out);
+      if (!s_place[tok[f]].live) v[f].a = v[f].b = make_uint4(0, 0, 0, 0);
+      else if (INT4) v[f] = Sixteen{values_of(v[f].a.x, v[f].a.z), values_of(v[f].a.y, v[f].a.z)};
+      dst[0] = v[f].a;
+      dst[1] = v[f].b;
     }
   }
 }
