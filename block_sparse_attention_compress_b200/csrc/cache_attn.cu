@@ -169,6 +169,11 @@ __device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs&
   return span_of<STEP>(len, a.n_new, r0 / a.G, (r1 - 1) / a.G, a.window);
 }
 
+__device__ __forceinline__ void check_length(const CacheArgs& c, const CacheAttnArgs& a, int b) {
+  const int len = __ldg(a.seqlens + b);
+  if (len < 0 || len > a.max_seqlen) cache::report(c.status);
+}
+
 // One tile of 16 tokens as a stage of the ring holds it.  4 bits: key codes, value codes, (s, z) pairs of
 // keys and of values; rows of values lie with their 16-byte units turned by the row, so that the
 // lanes' loads spread over the banks.  bf16: key rows, value rows, units turned likewise.
@@ -285,14 +290,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   char* sq = smem + W * kWarpBytes + rg * kQ;                     // this row group's queries
   float* sq_sc = reinterpret_cast<float*>(sq + NT * (NG + 1) * 512);
 
-  if (c.status) {   // lengths out of range are told of once
-    for (long long b = (long long)blockIdx.x * blockDim.x + threadIdx.x; b < c.batch; b += (long long)gridDim.x * blockDim.x) {
-      const int n = __ldg(a.seqlens + b);
-      if (n < 0 || n > a.max_seqlen) cache::report(c.status);
-    }
-  }
-
   // ---- which tiles are this block's: `left` of them from tile t of item (b, h, rt) on
+  asm volatile("griddepcontrol.launch_dependents;");   // the join may start to be set up
   int b, h, rt, t = 0;
   long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles
   if (pl.whole) {
@@ -301,6 +300,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     h = id % c.h_kv;
     b = id / c.h_kv;
     left = span_of<kStep>(c, a, pl, b, rt).tiles;
+    if (h == 0 && rt == 0 && threadIdx.x == 0) check_length(c, a, b);
   } else {
     const auto weight = [&](int bb) {
       long long w = 0;
@@ -310,7 +310,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     const int strip = (c.batch + W * 32 - 1) / (W * 32);
     const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
     long long mine = 0;
-    for (int x = b0; x < b1; ++x) mine += weight(x);
+    for (int x = b0; x < b1; ++x) {
+      mine += weight(x);
+      if (blockIdx.x == 0) check_length(c, a, x);
+    }
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -359,6 +362,66 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       cut.last = (int)((pos0 + sp.tiles - 1) / per);
       cut.rows = min(R - rt * pl.tile_rows, pl.tile_rows);
     }
+
+    // ---- this warp's run of tiles, [ta, tb) of the item
+    const int each = (take + streams - 1) / streams;
+    const int ta = t + min(take, ts * each), tb = t + min(take, (ts + 1) * each);
+    // steps inside [all_lo, all_hi) are seen whole by every row of the block
+    const int row_lo = rt * pl.tile_rows / a.G, row_hi = (min(R, (rt + 1) * pl.tile_rows) - 1) / a.G;
+    const int all_lo = a.window > 0 ? max(0, sp.p0 + row_hi - a.window + 1) : 0, all_hi = sp.p0 + row_lo + 1;
+
+    // the next tile to copy: its place in its page, and the page after that one, fetched ahead
+    int cp_u = sp.base + ta * kStep, cp_j = 0, cp_off = 0, ahead = 0;
+    const int cp_end = sp.base + tb * kStep;
+    bool here = false;      // the page is valid
+    uint32_t missing = 0;   // bit stage * U + x: tile x of that stage has no valid page
+    const int32_t* pages = c.page_table + (size_t)b * c.max_pages;
+    Walk<INT4, DK, DV> walk;
+    const auto open_page = [&](int page) {
+      here = page >= 0 && page < c.n_pages;
+      walk.go(c, here ? page : 0, cp_off, h, lane);
+      if (!here && lane == 0) cache::report(c.status);
+      // pages behind the last token are not looked up
+      const long long next = (long long)(cp_j + 1) * c.page_size;
+      ahead = next < min(sp.hi, cp_end) ? __ldg(pages + cp_j + 1) : -1;
+    };
+    if (ta < tb && sp.hi > 0) {
+      cp_j = cp_u / c.page_size;
+      cp_off = cp_u - cp_j * c.page_size;
+      open_page(__ldg(pages + cp_j));
+    } else {
+      walk.go(c, 0, 0, h, lane);
+    }
+    const auto copy_next = [&](int stage) {
+      if (cp_u < cp_end) {
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          const uint32_t dst = ring_u + (stage * U + x) * T::kBytes, bit = 1u << (stage * U + x);
+          if (here && cp_u >= sp.lo && cp_u + kTile <= sp.hi) {
+            walk.template copy<true>(c, dst, lane, 0, kTile);
+            missing &= ~bit;
+          } else {   // rows that do not exist are zeros, and masked
+            const bool some = here && cp_u < sp.hi;
+            walk.template copy<false>(c, dst, lane, some ? sp.lo - cp_u : 0, some ? sp.hi - cp_u : 0);
+            missing = some ? missing & ~bit : missing | bit;
+          }
+          cp_u += kTile;
+          cp_off += kTile;
+          if (cp_off < c.page_size) {
+            walk.next(c);
+          } else if (cp_u < min(sp.hi, cp_end)) {
+            cp_off = 0;
+            ++cp_j;
+            open_page(ahead);
+          } else {
+            here = false;
+          }
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) copy_next(s);
 
     // ---- queries as B fragments: row n = lane / 4 of each tile of 8.  4 bits: through shared memory
     uint32_t qf[INT4 ? 1 : NT][INT4 ? 1 : KS][2];
@@ -466,66 +529,6 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         max_s[gr] = 0;
       }
     }
-
-    // ---- this warp's run of tiles, [ta, tb) of the item
-    const int each = (take + streams - 1) / streams;
-    const int ta = t + min(take, ts * each), tb = t + min(take, (ts + 1) * each);
-    // steps inside [all_lo, all_hi) are seen whole by every row of the block
-    const int row_lo = rt * pl.tile_rows / a.G, row_hi = (min(R, (rt + 1) * pl.tile_rows) - 1) / a.G;
-    const int all_lo = a.window > 0 ? max(0, sp.p0 + row_hi - a.window + 1) : 0, all_hi = sp.p0 + row_lo + 1;
-
-    // the next tile to copy: its place in its page, and the page after that one, fetched ahead
-    int cp_u = sp.base + ta * kStep, cp_j = 0, cp_off = 0, ahead = 0;
-    const int cp_end = sp.base + tb * kStep;
-    bool here = false;      // the page is valid
-    uint32_t missing = 0;   // bit stage * U + x: tile x of that stage has no valid page
-    const int32_t* pages = c.page_table + (size_t)b * c.max_pages;
-    Walk<INT4, DK, DV> walk;
-    const auto open_page = [&](int page) {
-      here = page >= 0 && page < c.n_pages;
-      walk.go(c, here ? page : 0, cp_off, h, lane);
-      if (!here && lane == 0) cache::report(c.status);
-      // pages behind the last token are not looked up
-      const long long next = (long long)(cp_j + 1) * c.page_size;
-      ahead = next < min(sp.hi, cp_end) ? __ldg(pages + cp_j + 1) : -1;
-    };
-    if (ta < tb && sp.hi > 0) {
-      cp_j = cp_u / c.page_size;
-      cp_off = cp_u - cp_j * c.page_size;
-      open_page(__ldg(pages + cp_j));
-    } else {
-      walk.go(c, 0, 0, h, lane);
-    }
-    const auto copy_next = [&](int stage) {
-      if (cp_u < cp_end) {
-#pragma unroll
-        for (int x = 0; x < U; ++x) {
-          const uint32_t dst = ring_u + (stage * U + x) * T::kBytes, bit = 1u << (stage * U + x);
-          if (here && cp_u >= sp.lo && cp_u + kTile <= sp.hi) {
-            walk.template copy<true>(c, dst, lane, 0, kTile);
-            missing &= ~bit;
-          } else {   // rows that do not exist are zeros, and masked
-            const bool some = here && cp_u < sp.hi;
-            walk.template copy<false>(c, dst, lane, some ? sp.lo - cp_u : 0, some ? sp.hi - cp_u : 0);
-            missing = some ? missing & ~bit : missing | bit;
-          }
-          cp_u += kTile;
-          cp_off += kTile;
-          if (cp_off < c.page_size) {
-            walk.next(c);
-          } else if (cp_u < min(sp.hi, cp_end)) {
-            cp_off = 0;
-            ++cp_j;
-            open_page(ahead);
-          } else {
-            here = false;
-          }
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) copy_next(s);
 
     int stage = 0, since = 0;
     for (int tile = ta; tile < tb; ++tile) {
@@ -878,11 +881,12 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 constexpr int kJoinWarps = 8;
 template <int DV, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const Cut* __restrict__ cuts,
-                  const float2* __restrict__ part_ml, const float* __restrict__ part_o) {
+cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const Cut* cuts, const float2* part_ml,
+                  const float* part_o) {
   constexpr int kPer = DV / 32;
   __shared__ float s_acc[WPR > 1 ? kJoinWarps : 1][DV];
   __shared__ float2 s_ml[WPR > 1 ? kJoinWarps : 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // every thread, also of blocks with nothing to join
   const Cut cut = cuts[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
   const int rr = blockIdx.y * (kJoinWarps / WPR) + warp / WPR;
@@ -979,6 +983,22 @@ Parts parts_of(const CacheArgs& c, const Plan& p) {
   return x;
 }
 
+// The join waits on the device for the blocks that it reads from, so that its launch is behind it by then.
+template <int DV, int WPR>
+cudaError_t launch_join(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, const Cut* cuts, const float2* ml,
+                        const float* o, cudaStream_t st) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.blocks, (p.tile_rows * WPR + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<DV, WPR>, c, a, p, cuts, ml, o);
+}
+
 template <bool INT4, int DK, int DV, int NT, bool EXT>
 cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, cudaStream_t st) {
   using H = Shape<INT4, NT>;
@@ -999,11 +1019,8 @@ cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Pla
   if (e != cudaSuccess || p.whole) return e;
   // few items, many parts each: a block per row; else a warp per row
   const long long items = (long long)c.batch * c.h_kv * p.row_tiles;
-  if (items * 16 <= p.blocks)
-    cache_join_kernel<DV, kJoinWarps><<<dim3(p.blocks, p.tile_rows), kJoinWarps * 32, 0, st>>>(c, a, p, cuts, ml, o);
-  else
-    cache_join_kernel<DV, 1><<<dim3(p.blocks, (p.tile_rows + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, st>>>(c, a, p, cuts, ml, o);
-  return cudaGetLastError();
+  if (items * 16 <= p.blocks) return launch_join<DV, kJoinWarps>(c, a, p, cuts, ml, o, st);
+  return launch_join<DV, 1>(c, a, p, cuts, ml, o, st);
 }
 
 template <int DK, int DV>
