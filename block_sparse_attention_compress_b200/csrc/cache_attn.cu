@@ -140,8 +140,11 @@ constexpr float kNone = -3.0e38f;
 struct Plan {
   int row_tiles, tile_rows;   // row tiles per head and rows of one
   int blocks, min_tiles, row_groups;
+  int per_g;                  // r / G = r per_g >> 16 for the rows r < 256 of a call
+  int first[4], last[4];      // of each row tile: the first and the last new token it has rows of
   bool whole, nt2;
 };
+__device__ __forceinline__ int row_token(const Plan& p, int r) { return r * p.per_g >> 16; }
 
 // A block that holds the first part of an item cut over blocks says here which blocks hold the rest.
 struct Cut {
@@ -153,20 +156,18 @@ struct Span {
   int p0, lo, hi, base, tiles;
 };
 template <int STEP>
-__device__ __forceinline__ Span span_of(int len, int n_new, int i0, int i1, int window) {
+__device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, int b, int rt) {
   Span s;
-  s.p0 = len - n_new;
-  s.hi = max(0, s.p0 + i1 + 1);
-  s.lo = window > 0 ? max(0, s.p0 + i0 - window + 1) : 0;
+  s.p0 = min(max(__ldg(a.seqlens + b), 0), a.max_seqlen) - a.n_new;
+  s.hi = max(0, s.p0 + p.last[rt] + 1);
+  s.lo = a.window > 0 ? max(0, s.p0 + p.first[rt] - a.window + 1) : 0;
   s.base = s.lo & ~(kTile - 1);
   s.tiles = max(1, (s.hi - s.base + STEP - 1) / STEP);
   return s;
 }
-template <int STEP>
-__device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, int b, int rt) {
-  const int len = min(max(__ldg(a.seqlens + b), 0), a.max_seqlen);
-  const int r0 = rt * p.tile_rows, r1 = min(a.n_new * a.G, r0 + p.tile_rows);
-  return span_of<STEP>(len, a.n_new, r0 / a.G, (r1 - 1) / a.G, a.window);
+// a / b; 64-bit division is a hundred instructions
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 __device__ __forceinline__ void check_length(const CacheArgs& c, const CacheAttnArgs& a, int b) {
@@ -190,12 +191,15 @@ struct Stage {
   }
 };
 
-// 16 rows of ROW bytes that lie one behind the other, from the lane's place `src` on, to `at`(x) for unit x;
-// FULL: no row is left out
+// Tile copies are unrolled where all 16 rows exist (FULL), and short loops where some do not: code that
+// runs once a tile at most has to be fetched too, and a single token's call is mostly that.
+constexpr int copy_steps(bool full, int units) { return full ? (units + 31) / 32 : 1; }
+
+// 16 rows of ROW bytes that lie one behind the other, from the lane's place `src` on, to `at`(x) for unit x
 template <int ROW, bool FULL, class At>
 __device__ __forceinline__ void copy_run(const char* src, int lane, int lo, int hi, At at) {
   constexpr int kBytes = ROW % 16 == 0 ? 16 : 8, kAll = kTile * ROW / kBytes;
-#pragma unroll
+#pragma unroll copy_steps(FULL, kAll)
   for (int i = 0; i < (kAll + 31) / 32; ++i) {
     const int x = lane + 32 * i, row = x * kBytes / ROW;
     if (kAll % 32 == 0 || x < kAll) copy_async<kBytes>(at(x), src + 32 * i * kBytes, FULL || (row >= lo && row < hi));
@@ -206,7 +210,7 @@ __device__ __forceinline__ void copy_run(const char* src, int lane, int lo, int 
 template <int ROW, bool FULL, class Unit>
 __device__ __forceinline__ void copy_rows(uint32_t dst, const char* src, size_t stride, int lane, int lo, int hi, Unit unit) {
   constexpr int kUnits = ROW / 16, kAll = kTile * kUnits;
-#pragma unroll
+#pragma unroll copy_steps(FULL, kAll)
   for (int i = 0; i < kAll / 32; ++i) {
     const int x = lane + 32 * i, row = x / kUnits, u = x % kUnits;
     copy_async<16>(dst + row * ROW + unit(row, u) * 16, src + row * stride + u * 16, FULL || (row >= lo && row < hi));
@@ -328,7 +332,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       if (w < warp) upto += s_scan[w];
       total += s_scan[w];
     }
-    per = max((long long)pl.min_tiles, (total + gridDim.x - 1) / gridDim.x);
+    per = max((long long)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
     pos0 = per * blockIdx.x;
     if (pos0 >= total) {
       if (threadIdx.x == 0) cuts[blockIdx.x] = Cut{0, 0, -1, 0};
@@ -343,9 +347,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     }
     __syncthreads();
     b = s_b;
-    const long long head = weight(b) / c.h_kv;
-    h = (int)(s_off / head);
-    t = (int)(s_off % head);
+    int head = 0;   // tiles of a head, in all row tiles
+    for (int x = 0; x < pl.row_tiles; ++x) head += span_of<kStep>(c, a, pl, b, x).tiles;
+    h = (int)quotient(s_off, head);
+    t = (int)(s_off - (long long)h * head);
     rt = 0;
     for (int n; t >= (n = span_of<kStep>(c, a, pl, b, rt).tiles); ++rt) t -= n;
     left = min(per, total - pos0);
@@ -359,7 +364,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     if (t == 0 && take < sp.tiles) {
       cut.b = b;
       cut.head_tile = h * pl.row_tiles + rt;
-      cut.last = (int)((pos0 + sp.tiles - 1) / per);
+      cut.last = (int)quotient(pos0 + sp.tiles - 1, per);
       cut.rows = min(R - rt * pl.tile_rows, pl.tile_rows);
     }
 
@@ -367,8 +372,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     const int each = (take + streams - 1) / streams;
     const int ta = t + min(take, ts * each), tb = t + min(take, (ts + 1) * each);
     // steps inside [all_lo, all_hi) are seen whole by every row of the block
-    const int row_lo = rt * pl.tile_rows / a.G, row_hi = (min(R, (rt + 1) * pl.tile_rows) - 1) / a.G;
-    const int all_lo = a.window > 0 ? max(0, sp.p0 + row_hi - a.window + 1) : 0, all_hi = sp.p0 + row_lo + 1;
+        const int all_lo = a.window > 0 ? max(0, sp.p0 + pl.last[rt] - a.window + 1) : 0, all_hi = sp.p0 + pl.first[rt] + 1;
 
     // the next tile to copy: its place in its page, and the page after that one, fetched ahead
     int cp_u = sp.base + ta * kStep, cp_j = 0, cp_off = 0, ahead = 0;
@@ -420,7 +424,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       }
       cp_async_commit();
     };
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < S - 1; ++s) copy_next(s);
 
     // ---- queries as B fragments: row n = lane / 4 of each tile of 8.  4 bits: through shared memory
@@ -428,65 +432,64 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     float sc[NT][2];                    // what a column's raw score is multiplied by (natural units)
     int pos[NT][2];                     // the columns' positions
     float slope[EXT ? NT : 1][2];
-    if (!INT4 || ts == 0) {
+#pragma unroll(INT4 ? 1 : NT)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = min(r0 + nt * 8 + g8, R - 1), i = row_token(pl, r), g = r - i * a.G;
+      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
+      if constexpr (!INT4) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = min(r0 + nt * 8 + g8, R - 1), i = r / a.G, g = r - i * a.G;
-        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
-        if constexpr (!INT4) {
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
+          qf[nt][ks][0] = u.x;
+          qf[nt][ks][1] = u.y;
+        }
+      } else {
+        uint4 u[NG];
+        uint32_t top = 0;   // the largest |q| as bf16 bits, in both halves
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
-            qf[nt][ks][0] = u.x;
-            qf[nt][ks][1] = u.y;
+        for (int gr = 0; gr < NG; ++gr) {
+          u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
+          const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+        }
+        top = max(top & 0xffffu, top >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // a power of two that takes the row's largest query into [2^13, 2^14)
+        const int e2 = min(max(13 - ((int)(top >> 7) - 127), -120), 120);
+        const float up = pow2(e2);
+        uint4* frag = reinterpret_cast<uint4*>(sq) + nt * (NG + 1) * 32 + lane;
+        uint32_t* sums = reinterpret_cast<uint32_t*>(frag + NG * 32);
+        // (-8 sum, sum) of the groups' queries, each in two terms: one MMA's K holds eight groups' first
+        // terms and a second one the rest, or both terms of up to four groups; zeros where there is no group
+        if (ts == 0) {
+          if (NG < 4 && q4 >= NG) sums[0] = sums[1] = 0u;
+          if (NG > 4 && q4 + 4 >= NG) sums[1] = sums[3] = 0u;
+          // a query that is not finite makes its row NaN
+          if (q4 == 0) sq_sc[nt * 8 + g8] = top >= 0x7f80u ? NAN : fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f);
+        }
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+          if (gr % streams != ts) continue;   // the warps of a row group share the groups out
+          const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
+          float x[8], sum = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = cache::bf16_lo(w[e]) * up;
+            x[2 * e + 1] = cache::bf16_hi(w[e]) * up;
           }
-        } else {
-          uint4 u[NG];
-          float amax = 0.f, odd = 0.f;   // odd: NaN as soon as one query is not finite
 #pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
-            const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              amax = fmaxf(amax, fmaxf(fabsf(cache::bf16_lo(w[e])), fabsf(cache::bf16_hi(w[e]))));
-              odd = fmaf(cache::bf16_lo(w[e]), 0.f, fmaf(cache::bf16_hi(w[e]), 0.f, odd));
-            }
+          for (int e = 0; e < 8; ++e) sum += x[e];
+          frag[gr * 32] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1] * 0.0625f, x[5] * 0.0625f), pack_f16(x[2], x[6]),
+                                     pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
+          sum = warp_sum4(sum) * 0x1p-24f;   // the products carry 2^-24: so do the sums beside them
+          if (gr % 4 == q4) {
+            const float first = __bfloat162float(__float2bfloat16_rn(sum)), rest = sum - first;
+            const uint32_t t0 = pack_bf16(-8.f * first, first), t1 = pack_bf16(-8.f * rest, rest);
+            sums[gr / 4] = t0;
+            sums[NG <= 4 ? 1 : 2 + gr / 4] = t1;
           }
-          amax = warp_max4(amax);
-          odd = warp_sum4(odd);
-          // a power of two that takes the row's largest query into [2^13, 2^14)
-          const int e2 = min(max(13 - ((int)((__float_as_uint(amax) >> 23) & 255u) - 127), -120), 120);
-          const float up = pow2(e2);
-          float sums[2] = {0.f, 0.f};   // of groups q4 and q4 + 4
-          uint4* frag = reinterpret_cast<uint4*>(sq) + nt * (NG + 1) * 32 + lane;
-#pragma unroll
-          for (int gr = 0; gr < NG; ++gr) {
-            const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
-            float x[8], sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[2 * e] = cache::bf16_lo(w[e]) * up;
-              x[2 * e + 1] = cache::bf16_hi(w[e]) * up;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum += x[e];
-            frag[gr * 32] = make_uint4(pack_f16(x[0], x[4]), pack_f16(x[1] * 0.0625f, x[5] * 0.0625f), pack_f16(x[2], x[6]),
-                                       pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
-            sum = warp_sum4(sum) * 0x1p-24f;   // the products carry 2^-24: so do the sums beside them
-            if (gr % 4 == q4) sums[gr / 4] = sum;
-          }
-          // (-8 sum, sum) of the groups' queries, each in two terms: one MMA's K holds eight groups' first
-          // terms and a second one the rest, or both terms of up to four groups
-          uint32_t term[2][2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float top = __bfloat162float(__float2bfloat16_rn(sums[x])), rest = sums[x] - top;
-            term[0][x] = pack_bf16(-8.f * top, top);
-            term[1][x] = pack_bf16(-8.f * rest, rest);
-          }
-          frag[NG * 32] = make_uint4(term[0][0], NG <= 4 ? term[1][0] : term[0][1], term[1][0], term[1][1]);
-          if (q4 == 0) sq_sc[nt * 8 + g8] = fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f) + odd;
         }
       }
     }
@@ -495,7 +498,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int rc = min(r0 + nt * 8 + 2 * q4 + j, R - 1), ic = rc / a.G;
+        const int rc = min(r0 + nt * 8 + 2 * q4 + j, R - 1), ic = row_token(pl, rc);
         sc[nt][j] = INT4 ? sq_sc[nt * 8 + 2 * q4 + j] : a.scale;
         pos[nt][j] = sp.p0 + ic;
         if constexpr (EXT) slope[nt][j] = a.slopes ? __ldg(a.slopes + h * a.G + rc - ic * a.G) * kLog2e : 0.f;
@@ -849,7 +852,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         acc.x += k * y.x; acc.y += k * y.y; acc.z += k * y.z; acc.w += k * y.w;
       }
       if (alone) {
-        const int i = r / a.G;
+        const int i = row_token(pl, r);
         const size_t row = ((size_t)b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
         const float inv = ll > 0.f ? 1.f / ll : ll;   // a NaN stays one; nothing attended: zeros
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + d) =
@@ -893,6 +896,16 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
   if (cut.last < 0 || rr >= cut.rows) return;   // WPR > 1: the whole block
   const int n = cut.last - (int)blockIdx.x + 1;   // parts: slot 1 of this block, slot 0 of the next ones
   const auto at = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0)) * pl.tile_rows + rr; };
+  const auto fetch = [&](int i, float (&v)[kPer]) {
+    const float* y = part_o + at(i) * DV + lane * kPer;
+    if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y);
+  };
+  constexpr int kAhead = 4;   // parts of this warp on their way at once; the first before the maxima are known
+  float v[kAhead][kPer];
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x)
+    if (sub + x * WPR < n) fetch(sub + x * WPR, v[x]);
   float mm = kNone;
   for (int i = lane; i < n; i += 32) mm = fmaxf(mm, part_ml[at(i)].x);
 #pragma unroll
@@ -900,17 +913,21 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
   float ll = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = sub; i < n; i += WPR) {
-    const float2 ml = part_ml[at(i)];
-    const float k = ex2(ml.x - mm);
-    ll += k * ml.y;
-    const float* y = part_o + at(i) * DV + lane * kPer;
-    float v[kPer];
-    if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y);
-    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y);
+  for (int i0 = sub; i0 < n; i0 += kAhead * WPR) {
+    if (i0 != sub) {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] += k * v[e];
+      for (int x = 0; x < kAhead; ++x)
+        if (i0 + x * WPR < n) fetch(i0 + x * WPR, v[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      if (i0 + x * WPR >= n) break;
+      const float2 ml = part_ml[at(i0 + x * WPR)];
+      const float k = ex2(ml.x - mm);
+      ll += k * ml.y;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += k * v[x][e];
+    }
   }
   if constexpr (WPR > 1) {
 #pragma unroll
@@ -925,7 +942,7 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
       for (int e = 0; e < kPer; ++e) acc[e] += s_acc[warp + w][lane * kPer + e];
     }
   }
-  const int h = cut.head_tile / pl.row_tiles, r = cut.head_tile % pl.row_tiles * pl.tile_rows + rr, i = r / a.G;
+  const int h = cut.head_tile / pl.row_tiles, r = cut.head_tile % pl.row_tiles * pl.tile_rows + rr, i = row_token(pl, r);
   const size_t row = ((size_t)cut.b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
   const float inv = ll > 0.f ? 1.f / ll : ll;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + lane * kPer);
@@ -947,7 +964,7 @@ auto with_shape(bool int4, bool nt2, F f) {
 }
 
 constexpr int kSms = 148;
-constexpr int kWholeTokens = 512;   // items up to this length are not cut
+constexpr int kWholeTokens = 256;   // a warp's share of items that are not cut: a second kernel costs 6 us
 
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   Plan p;
@@ -958,12 +975,17 @@ Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   p.row_groups = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   p.tile_rows = (p.nt2 ? 16 : 8) * p.row_groups;
   p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
+  p.per_g = (65536 + a.G - 1) / a.G;
+  for (int rt = 0; rt < p.row_tiles; ++rt) {   // R <= 256: at most four tiles, of 64 rows
+    p.first[rt] = rt * p.tile_rows / a.G;
+    p.last[rt] = (std::min(R, (rt + 1) * p.tile_rows) - 1) / a.G;
+  }
   // the most tiles an item can have
   long long range = a.max_seqlen;
   if (a.window > 0) range = std::min<long long>(range, (long long)a.window + a.n_new + kTile);
   const long long tiles = (range + step - 1) / step, items = (long long)c.batch * c.h_kv * p.row_tiles;
   p.min_tiles = 2 * (W / p.row_groups);
-  p.whole = range <= kWholeTokens;
+  p.whole = range <= kWholeTokens * (W / p.row_groups);
   const long long most = (long long)kSms * resident;
   // items <= 2^31 (cache_attn_fits), tiles <= 2^26
   p.blocks = (int)(p.whole ? std::min<long long>(items, INT32_MAX) : std::min(most, (items * tiles + p.min_tiles - 1) / p.min_tiles));
