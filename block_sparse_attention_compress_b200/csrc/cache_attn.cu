@@ -38,6 +38,7 @@ namespace nsa {
 namespace {
 
 constexpr int kTile = 16;         // tokens per step of a warp
+constexpr int kLonger = 2;        // see the cutting of the work
 constexpr int kFlush = 32;        // tiles between two corrections of the accumulators
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -88,6 +89,7 @@ __device__ __forceinline__ float2 mul2(float a, float b, float f) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_pack(a, b)), "l"(f2_pack(f, f)));
   return f2_unpack(d);
 }
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }   // of a normal one
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
 
 // copies of 8 or 16 bytes into shared memory; `on` false: zeros
@@ -297,7 +299,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   // ---- which tiles are this block's: `left` of them from tile t of item (b, h, rt) on
   asm volatile("griddepcontrol.launch_dependents;");   // the join may start to be set up
   int b, h, rt, t = 0;
-  long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles
+  long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles (whole_runs: of the run)
+  bool whole_runs = false;
   if (pl.whole) {
     int id = blockIdx.x;
     rt = id % pl.row_tiles; id /= pl.row_tiles;
@@ -306,54 +309,85 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     left = span_of<kStep>(c, a, pl, b, rt).tiles;
     if (h == 0 && rt == 0 && threadIdx.x == 0) check_length(c, a, b);
   } else {
-    const auto weight = [&](int bb) {
+    // tiles of an item in runs of `unit`, and those of a sequence's items
+    const auto units = [&](int bb, int x, long long unit) {
+      const int n = span_of<kStep>(c, a, pl, bb, x).tiles;
+      return unit == 1 ? n : (int)quotient(n + unit - 1, unit);
+    };
+    const auto weight = [&](int bb, long long unit) {
       long long w = 0;
-      for (int x = 0; x < pl.row_tiles; ++x) w += span_of<kStep>(c, a, pl, bb, x).tiles;
+      for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x, unit);
       return w * c.h_kv;
     };
     const int strip = (c.batch + W * 32 - 1) / (W * 32);
     const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
-    long long mine = 0;
+    // the strips' sums: of those before this thread's, and of all
+    const auto scan = [&](long long mine, long long& total) {
+      long long upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      if (lane == 31) s_scan[warp] = upto;
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w < warp) upto += s_scan[w];
+        total += s_scan[w];
+      }
+      __syncthreads();
+      return upto - mine;
+    };
+    long long mine = 0, total;
     for (int x = b0; x < b1; ++x) {
-      mine += weight(x);
+      mine += weight(x, 1);
       if (blockIdx.x == 0) check_length(c, a, x);
     }
-    long long upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
-    }
-    if (lane == 31) s_scan[warp] = upto;
-    __syncthreads();
-    long long total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) upto += s_scan[w];
-      total += s_scan[w];
-    }
+    long long before = scan(mine, total);
     per = max((long long)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
-    pos0 = per * blockIdx.x;
+    // Runs that end with their item spare a block the second half of its work that the end of one item and
+    // the start of the next are (queries, first copies and join: about 6 us); they are longer, since items end
+    // inside the last run.  Longer by no more than kLonger steps a warp: that is the cheaper cut (64 items of
+    // 1100 tokens 15.6 us instead of 18.6), but for a few items, where finding the runs costs more.
+    const long long items = (long long)c.batch * c.h_kv * pl.row_tiles, spare = gridDim.x - items;
+    if (spare > 0 && items >= 16) {
+      const long long longer = max((long long)pl.min_tiles, quotient(total + spare - 1, spare));
+      whole_runs = longer - per <= kLonger * streams;
+      if (whole_runs) {
+        per = longer;
+        mine = 0;
+        for (int x = b0; x < b1; ++x) mine += weight(x, per);
+        before = scan(mine, total);   // in runs: sum over items of ceil(tiles / per) <= spare + items
+      }
+    }
+    pos0 = whole_runs ? blockIdx.x : per * blockIdx.x;
     if (pos0 >= total) {
       if (threadIdx.x == 0) cuts[blockIdx.x] = Cut{0, 0, -1, 0};
       return;
     }
-    if (upto - mine <= pos0 && pos0 < upto) {
-      long long off = pos0 - (upto - mine);
+    const long long unit = whole_runs ? per : 1;
+    if (before <= pos0 && pos0 < before + mine) {
+      long long off = pos0 - before;
       int x = b0;
-      for (long long w; off >= (w = weight(x)); ++x) off -= w;
+      for (long long w; off >= (w = weight(x, unit)); ++x) off -= w;
       s_b = x;
       s_off = off;
     }
     __syncthreads();
     b = s_b;
-    int head = 0;   // tiles of a head, in all row tiles
-    for (int x = 0; x < pl.row_tiles; ++x) head += span_of<kStep>(c, a, pl, b, x).tiles;
+    int head = 0;   // units of a head, in all row tiles
+    for (int x = 0; x < pl.row_tiles; ++x) head += units(b, x, unit);
     h = (int)quotient(s_off, head);
     t = (int)(s_off - (long long)h * head);
     rt = 0;
-    for (int n; t >= (n = span_of<kStep>(c, a, pl, b, rt).tiles); ++rt) t -= n;
+    for (int n; t >= (n = units(b, rt, unit)); ++rt) t -= n;
     left = min(per, total - pos0);
+    if (whole_runs) {
+      t *= (int)per;
+      left = min(per, (long long)span_of<kStep>(c, a, pl, b, rt).tiles - t);
+    }
   }
 
   Cut cut{0, 0, -1, 0};
@@ -364,7 +398,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     if (t == 0 && take < sp.tiles) {
       cut.b = b;
       cut.head_tile = h * pl.row_tiles + rt;
-      cut.last = (int)quotient(pos0 + sp.tiles - 1, per);
+      cut.last = (int)(whole_runs ? blockIdx.x + quotient(sp.tiles - 1, per) : quotient(pos0 + sp.tiles - 1, per));
       cut.rows = min(R - rt * pl.tile_rows, pl.tile_rows);
     }
 
@@ -667,7 +701,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
             x = x ? x | 0x7fu : 0u;             // all of the binade
             // s 2^k < 2^7: k = 6 - (exponent of s)
             const float to = pow2(x ? min(6 - ((int)(x >> 7) - 127), 100) : 100);
-            grow[gr] = to / top_s[gr];
+            grow[gr] = to * inverse_pow2(top_s[gr]);
             top_s[gr] = to;
             max_s[gr] = x;
           }
@@ -802,6 +836,12 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     float* s_o = reinterpret_cast<float*>(ring);   // [kCols][kRow], then maxima and sums
     float* s_m = s_o + kCols * kRow;
     float* s_l = s_m + kCols;
+    if (ta >= tb) {   // no tiles: its sums are not read
+      if (lane < kCols) {
+        s_m[lane] = kNone;
+        s_l[lane] = 0.f;
+      }
+    } else
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -820,7 +860,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
             float z = zacc[nt][gr][j];
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-            const float down = 1.f / top_s[gr];   // powers of two
+            const float down = inverse_pow2(top_s[gr]);
             *reinterpret_cast<float4*>(row + 32 * gr + 4 * g8) =
                 make_float4(fmaf(o[2 * gr][nt][j] * 0x1p24f, down, z), fmaf(o[2 * gr][nt][j + 2] * 0x1p20f, down, z),
                             fmaf(o[2 * gr + 1][nt][j] * 0x1p24f, down, z), fmaf(o[2 * gr + 1][nt][j + 2] * 0x1p20f, down, z));
@@ -846,9 +886,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = 0; w < streams; ++w) {
         const float* f = reinterpret_cast<const float*>(base + w * step);
-        const float k = ex2(f[kCols * kRow + col] - mm);
+        const float lw = f[kCols * kRow + kCols + col], k = ex2(f[kCols * kRow + col] - mm);
+        if (lw == 0.f) continue;
         const float4 y = *reinterpret_cast<const float4*>(f + col * kRow + d);
-        ll += k * f[kCols * kRow + kCols + col];
+        ll += k * lw;
         acc.x += k * y.x; acc.y += k * y.y; acc.z += k * y.z; acc.w += k * y.w;
       }
       if (alone) {
@@ -964,7 +1005,8 @@ auto with_shape(bool int4, bool nt2, F f) {
 }
 
 constexpr int kSms = 148;
-constexpr int kWholeTokens = 256;   // a warp's share of items that are not cut: a second kernel costs 6 us
+// A warp's share of items that are not cut: the second kernel costs 5 us, so does a share of 128 tokens
+constexpr int kWholeTokens = 128;
 
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   Plan p;
@@ -985,7 +1027,7 @@ Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   if (a.window > 0) range = std::min<long long>(range, (long long)a.window + a.n_new + kTile);
   const long long tiles = (range + step - 1) / step, items = (long long)c.batch * c.h_kv * p.row_tiles;
   p.min_tiles = 2 * (W / p.row_groups);
-  p.whole = range <= kWholeTokens * (W / p.row_groups);
+  p.whole = range <= kWholeTokens * (W / p.row_groups) * (items >= 64 ? 2 : 1);
   const long long most = (long long)kSms * resident;
   // items <= 2^31 (cache_attn_fits), tiles <= 2^26
   p.blocks = (int)(p.whole ? std::min<long long>(items, INT32_MAX) : std::min(most, (items * tiles + p.min_tiles - 1) / p.min_tiles));
