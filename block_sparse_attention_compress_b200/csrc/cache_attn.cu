@@ -38,7 +38,7 @@ namespace nsa {
 namespace {
 
 constexpr int kTile = 16;         // tokens per step of a warp
-constexpr int kLonger = 2;        // see the cutting of the work
+constexpr int kShort = 8, kLonger = 2;   // see the cutting of the work
 constexpr int kFlush = 32;        // tiles between two corrections of the accumulators
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -298,6 +298,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 
   // ---- which tiles are this block's: `left` of them from tile t of item (b, h, rt) on
   asm volatile("griddepcontrol.launch_dependents;");   // the join may start to be set up
+  // a step of all streams is 1.3 us (4 bits), a part's start and end about 5
+  const int extra = 4 * streams;
   int b, h, rt, t = 0;
   long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles (whole_runs: of the run)
   bool whole_runs = false;
@@ -306,13 +308,14 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     rt = id % pl.row_tiles; id /= pl.row_tiles;
     h = id % c.h_kv;
     b = id / c.h_kv;
-    left = span_of<kStep>(c, a, pl, b, rt).tiles;
+    left = (long long)span_of<kStep>(c, a, pl, b, rt).tiles + extra;
     if (h == 0 && rt == 0 && threadIdx.x == 0) check_length(c, a, b);
   } else {
-    // tiles of an item in runs of `unit`, and those of a sequence's items
+    // An item's share of the work: its tiles and, before them, what its start costs in tiles (unit 0); or
+    // its runs of `unit` tiles.  And that of a sequence's items.
     const auto units = [&](int bb, int x, long long unit) {
       const int n = span_of<kStep>(c, a, pl, bb, x).tiles;
-      return unit == 1 ? n : (int)quotient(n + unit - 1, unit);
+      return unit == 0 ? n + extra : (int)quotient(n + unit - 1, unit);
     };
     const auto weight = [&](int bb, long long unit) {
       long long w = 0;
@@ -342,19 +345,19 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     };
     long long mine = 0, total;
     for (int x = b0; x < b1; ++x) {
-      mine += weight(x, 1);
+      mine += weight(x, 0);
       if (blockIdx.x == 0) check_length(c, a, x);
     }
     long long before = scan(mine, total);
     per = max((long long)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
-    // Runs that end with their item spare a block the second half of its work that the end of one item and
-    // the start of the next are (queries, first copies and join: about 6 us); they are longer, since items end
-    // inside the last run.  Longer by no more than kLonger steps a warp: that is the cheaper cut (64 items of
-    // 1100 tokens 15.6 us instead of 18.6), but for a few items, where finding the runs costs more.
+    // Runs that end with their item spare a block the end of one item and the start of the next (about 5 us),
+    // but are longer, since items end inside their last run.  While a run is short, that is the cheaper
+    // cut (64 items of 1100 tokens 15.6 us instead of 18.6); long runs hide those behind the SM's other
+    // blocks, and for a few items finding the runs costs more.
     const long long items = (long long)c.batch * c.h_kv * pl.row_tiles, spare = gridDim.x - items;
     if (spare > 0 && items >= 16) {
       const long long longer = max((long long)pl.min_tiles, quotient(total + spare - 1, spare));
-      whole_runs = longer - per <= kLonger * streams;
+      whole_runs = longer <= kShort * streams && longer - per <= kLonger * streams;
       if (whole_runs) {
         per = longer;
         mine = 0;
@@ -367,7 +370,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       if (threadIdx.x == 0) cuts[blockIdx.x] = Cut{0, 0, -1, 0};
       return;
     }
-    const long long unit = whole_runs ? per : 1;
+    const long long unit = whole_runs ? per : 0;
     if (before <= pos0 && pos0 < before + mine) {
       long long off = pos0 - before;
       int x = b0;
@@ -385,26 +388,55 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     for (int n; t >= (n = units(b, rt, unit)); ++rt) t -= n;
     left = min(per, total - pos0);
     if (whole_runs) {
-      t *= (int)per;
-      left = min(per, (long long)span_of<kStep>(c, a, pl, b, rt).tiles - t);
+      t = t * (int)per + extra;
+      left = min(per, (long long)span_of<kStep>(c, a, pl, b, rt).tiles + extra - t);
     }
   }
 
   Cut cut{0, 0, -1, 0};
   while (left > 0) {
     const Span sp = span_of<kStep>(c, a, pl, b, rt);
-    const int take = (int)min(left, (long long)(sp.tiles - t));
+    // the block's part of the item's share, [t, t + part), and its tiles in that
+    const int part = (int)min(left, (long long)(sp.tiles + extra - t)), first = max(0, t - extra);
+    const int take = max(0, t + part - extra) - first;
     const int r0 = rt * pl.tile_rows + rg * kCols;   // this warp's first row (maybe behind the last)
-    if (t == 0 && take < sp.tiles) {
+    const auto next_item = [&] {
+      left -= part;
+      pos0 += part;
+      t = 0;
+      if (++rt == pl.row_tiles) {
+        rt = 0;
+        if (++h == c.h_kv) {
+          h = 0;
+          ++b;
+        }
+      }
+    };
+    const int tile_rows = min(R - rt * pl.tile_rows, pl.tile_rows);
+    const auto out_row = [&](int r) {   // of the item's row r, among all
+      const int i = row_token(pl, r);
+      return ((size_t)b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
+    };
+    if (take == 0) break;   // the run ends before the item's first tile
+    if (sp.hi == 0) {       // an empty sequence
+      for (int x = threadIdx.x; x < tile_rows * (DV / 4); x += W * 32) {
+        const size_t row = out_row(rt * pl.tile_rows + x / (DV / 4));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + (x % (DV / 4)) * 4) = make_uint2(0, 0);
+        if (a.lse && x % (DV / 4) == 0) a.lse[row] = -INFINITY;
+      }
+      next_item();
+      continue;
+    }
+    if (first == 0 && take < sp.tiles) {
       cut.b = b;
       cut.head_tile = h * pl.row_tiles + rt;
-      cut.last = (int)(whole_runs ? blockIdx.x + quotient(sp.tiles - 1, per) : quotient(pos0 + sp.tiles - 1, per));
-      cut.rows = min(R - rt * pl.tile_rows, pl.tile_rows);
+      cut.last = (int)(whole_runs ? blockIdx.x + quotient(sp.tiles - 1, per) : quotient(pos0 - t + extra + sp.tiles - 1, per));
+      cut.rows = tile_rows;
     }
 
     // ---- this warp's run of tiles, [ta, tb) of the item
     const int each = (take + streams - 1) / streams;
-    const int ta = t + min(take, ts * each), tb = t + min(take, (ts + 1) * each);
+    const int ta = first + min(take, ts * each), tb = first + min(take, (ts + 1) * each);
     // steps inside [all_lo, all_hi) are seen whole by every row of the block
         const int all_lo = a.window > 0 ? max(0, sp.p0 + pl.last[rt] - a.window + 1) : 0, all_hi = sp.p0 + pl.first[rt] + 1;
 
@@ -874,8 +906,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       }
     __syncthreads();
     const bool alone = take == sp.tiles;   // else: to the slot of a run that begins (1) or continues (0) the item
-    const size_t slot = (size_t)blockIdx.x * 2 + (t == 0);
-    const int tile_rows = min(R - rt * pl.tile_rows, pl.tile_rows);
+    const size_t slot = (size_t)blockIdx.x * 2 + (first == 0);
     for (int x = threadIdx.x; x < tile_rows * (DV / 4); x += W * 32) {
       const int rr = x / (DV / 4), d = (x % (DV / 4)) * 4, col = rr % kCols, r = rt * pl.tile_rows + rr;
       const char* base = smem + (rr / kCols) * kWarpBytes;   // the first warp of the row's group
@@ -893,8 +924,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         acc.x += k * y.x; acc.y += k * y.y; acc.z += k * y.z; acc.w += k * y.w;
       }
       if (alone) {
-        const int i = row_token(pl, r);
-        const size_t row = ((size_t)b * a.n_new + i) * a.h_q + h * a.G + (r - i * a.G);
+        const size_t row = out_row(r);
         const float inv = ll > 0.f ? 1.f / ll : ll;   // a NaN stays one; nothing attended: zeros
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * DV + d) =
             make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
@@ -905,16 +935,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         if (d == 0) part_ml[row] = make_float2(mm, ll);
       }
     }
-    left -= take;
-    pos0 += take;
-    t = 0;
-    if (++rt == pl.row_tiles) {
-      rt = 0;
-      if (++h == c.h_kv) {
-        h = 0;
-        ++b;
-      }
-    }
+    next_item();
     if (left > 0) __syncthreads();   // the next item's copies reuse the ring
   }
   if (!pl.whole && threadIdx.x == 0) cuts[blockIdx.x] = cut;
@@ -992,13 +1013,20 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
   if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
-// Warps per block, blocks per SM, tiles of 16 tokens per step and stages of the ring.
+// Warps per block, blocks per SM, tiles of 16 tokens per step.
 template <bool INT4, int NT>
 struct Shape {
   static constexpr int W = INT4 ? 4 : 8;
   static constexpr int B = INT4 ? (NT == 2 ? 2 : 4) : 1;
-  static constexpr int U = INT4 ? 2 : 1, S = INT4 && NT == 2 ? 3 : 2;
+  static constexpr int U = INT4 ? 2 : 1;
 };
+// Stages of the ring: as many as fit beside the other blocks of the SM, at most 4 (4 bits: 3).
+template <bool INT4, int DK, int DV, int NT>
+constexpr int stages() {
+  using H = Shape<INT4, NT>;
+  constexpr int room = 227 * 1024 / H::B - 1024 - 1024 - query_smem<INT4, DK, NT>();
+  return std::min(INT4 ? 3 : 4, room / (H::W * H::U * Stage<INT4, DK, DV>::kBytes));
+}
 template <class F>
 auto with_shape(bool int4, bool nt2, F f) {
   return int4 ? (nt2 ? f(Shape<true, 2>()) : f(Shape<true, 1>())) : nt2 ? f(Shape<false, 2>()) : f(Shape<false, 1>());
@@ -1066,11 +1094,12 @@ cudaError_t launch_join(const CacheArgs& c, const CacheAttnArgs& a, const Plan& 
 template <bool INT4, int DK, int DV, int NT, bool EXT>
 cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, cudaStream_t st) {
   using H = Shape<INT4, NT>;
-  constexpr int kRing = H::W * warp_smem<INT4, DK, DV, NT, H::U, H::S>(), kQ = query_smem<INT4, DK, NT>();
-  static_assert((kRing + kQ + 2048) * H::B <= 228 * 1024, "the rings of the resident blocks fit an SM");
+  constexpr int S = stages<INT4, DK, DV, NT>();
+  constexpr int kRing = H::W * warp_smem<INT4, DK, DV, NT, H::U, S>(), kQ = query_smem<INT4, DK, NT>();
+  static_assert(S >= 2 && (kRing + kQ + 2048) * H::B <= 228 * 1024, "the rings of the resident blocks fit an SM");
   static_assert(kRing + 4 * kQ <= 227 * 1024, "a block's shared memory");
   static PerDevice set;
-  auto* f = cache_attn_kernel<INT4, DK, DV, NT, H::W, H::B, H::U, H::S, EXT>;
+  auto* f = cache_attn_kernel<INT4, DK, DV, NT, H::W, H::B, H::U, S, EXT>;
   cudaError_t e = set.once([&] { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 4 * kQ); });
   if (e != cudaSuccess) return e;
   const Parts x = parts_of(c, p);
