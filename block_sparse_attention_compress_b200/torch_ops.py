@@ -211,8 +211,11 @@ class KVCache:
             raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {self.device}")
         return t.data_ptr()
 
-    def _new(self, shape, dtype, stream):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+    def _new(self, like, shape, stream, dtype=torch.bfloat16):
+        if like.shape == shape and dtype is like.dtype:   # the quickest of torch's ways
+            t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        else:
+            t = like.new_empty(shape, dtype=dtype)
         if stream is not None:   # torch must not hand the memory out again before that stream is done
             t.record_stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
         return t
@@ -246,8 +249,10 @@ class KVCache:
             if q.shape[:-2] != lead:
                 raise ValueError("q must hold the same tokens as k")
             if q_out is None:
-                q_out = self._new(q.shape, torch.bfloat16, stream)
-            a.q, a.q_out, a.h_q = q.data_ptr(), self._like(q_out, q.shape, torch.bfloat16, "q_out"), h_q
+                q_out = self._new(q, q.shape, stream)
+            else:
+                self._like(q_out, q.shape, torch.bfloat16, "q_out")
+            a.q, a.q_out, a.h_q = q.data_ptr(), q_out.data_ptr(), h_q
         if lead.numel():   # no tokens: nothing to do
             self._call(nsa_cache_append, stream, a)
         return q_out if q is not None else None
@@ -265,11 +270,17 @@ class KVCache:
         if lead[-1] < 0:
             raise ValueError("read takes a number of tokens")
         shapes = (*lead, self.h_kv, self.d_k), (*lead, self.h_kv, self.d_v)
-        k_out = self._new(shapes[0], torch.bfloat16, stream) if k_out is None else k_out
-        v_out = self._new(shapes[1], torch.bfloat16, stream) if v_out is None else v_out
-        k_ptr, v_ptr = self._like(k_out, shapes[0], torch.bfloat16, "k_out"), self._like(v_out, shapes[1], torch.bfloat16, "v_out")
+        if k_out is None:
+            k_out = self._new(seqlens, shapes[0], stream, torch.bfloat16)
+        else:
+            self._like(k_out, shapes[0], torch.bfloat16, "k_out")
+        if v_out is None:
+            v_out = self._new(k_out, shapes[1], stream)
+        else:
+            self._like(v_out, shapes[1], torch.bfloat16, "v_out")
         if lead[-1]:
-            self._call(nsa_cache_read, stream, seqlens, cu_seqlens, 0 if packed else lead[1], lead[0] if packed else 0, k_ptr, v_ptr)
+            self._call(nsa_cache_read, stream, seqlens, cu_seqlens, 0 if packed else lead[1], lead[0] if packed else 0, k_out.data_ptr(),
+                       v_out.data_ptr())
         return k_out, v_out
 
     def attend(self, q, seqlens, max_seqlen=None, *, softmax_scale=0.0, softcap=0.0, slopes=None, window=0, out=None,
@@ -285,8 +296,9 @@ class KVCache:
             raise ValueError(f"q: contiguous bf16 [{self.batch}, n, h_q, {self.d_k}] on {self.device}")
         B, n, h_q, _ = q.shape
         if out is None:
-            out = self._new((B, n, h_q, self.d_v), torch.bfloat16, stream)
-        out_ptr = self._like(out, (B, n, h_q, self.d_v), torch.bfloat16, "out")
+            out = self._new(q, (B, n, h_q, self.d_v), stream)
+        else:
+            self._like(out, (B, n, h_q, self.d_v), torch.bfloat16, "out")
         max_seqlen = self.max_len if max_seqlen is None else max_seqlen
         a = NsaCacheAttentionArgs(self._lengths(seqlens, self.batch, "seqlens"),
                                   None if slopes is None else self._like(slopes, (h_q,), torch.float32, "slopes"),
@@ -300,10 +312,10 @@ class KVCache:
                     self._workspaces.clear()
                 need = self._workspaces[key] = nsa_cache_attention_workspace(self.desc, a)
             if need:
-                workspace = self._new((need,), torch.uint8, stream)
+                workspace = self._new(q, (need,), stream, torch.uint8)
         if workspace is not None:
             a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        self._call(nsa_cache_attention, stream, q.data_ptr(), a, out_ptr)
+        self._call(nsa_cache_attention, stream, q.data_ptr(), a, out.data_ptr())
         return out
 
     def attend_workspace(self, n, h_q, max_seqlen=None, window=0):
