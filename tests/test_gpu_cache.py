@@ -393,6 +393,58 @@ def test_attention_long_sequence_beside_short_ones(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("B,h_kv,G,n_new,top,window,dk,dv", [
+    (2, 1, 16, 16, 3000, 0, 192, 128),      # 256 rows a head: four row tiles, cut sequences
+    (2, 1, 16, 16, 3000, 333, 128, 128),
+    (3, 1, 8, 4, 2500, 0, 64, 64),          # 32 rows: two row groups
+    (3, 2, 7, 5, 2500, 700, 64, 64),        # 35 rows: four row groups, the last ones partly empty
+    (70, 1, 3, 1, 1100, 0, 64, 64),         # runs that end with their items
+    (40, 8, 1, 1, 3000, 0, 64, 64),         # runs that do not
+    (20, 16, 2, 1, 6000, 2000, 64, 64),
+])
+def test_attention_cut_over_blocks(fmt, B, h_kv, G, n_new, top, window, dk, dv):
+    """Work that is shared out over blocks in runs, with empty and short sequences between the long ones."""
+    g = gen(B + top)
+    lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    lens[0], lens[-1] = top, top - 1
+    if B > 3:
+        lens[1], lens[2] = 0, 1
+    _, q, held, out, lse, _ = run_attention(fmt, dk, dv, 16, h_kv, G, lens, n_new, seed=B, window=window)
+    picks = list(range(B)) if B < 5 else [0, 1, 2, B // 2, B - 2, B - 1]
+    check_attention(out[picks], lse[picks], q[picks], [held[b] for b in picks], [lens[b] for b in picks], window=window)
+    assert torch.isfinite(out.float()).all() and not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("shape", ["rising", "falling", "offset", "mixed"])
+def test_four_bit_values_of_changing_scales(shape):
+    """A warp's long run over values whose scales grow or shrink by tokens and groups, or whose offsets dwarf
+    their spans, with weights from flat to steep: the accumulators' common factors have to follow."""
+    g = gen(30)
+    B, h_kv, L, d = 80, 8, 3000, 128
+    k, v = bf((L, 1, d), g), bf((L, 1, d), g)
+    f = torch.arange(L).float()[:, None, None]
+    if shape == "rising":
+        v = (v.float() * torch.exp2(f * (16 / L))).bfloat16()
+    elif shape == "falling":
+        v = (v.float() * torch.exp2(-f * (16 / L))).bfloat16()
+    elif shape == "offset":
+        v = (v.float() * 0.02 + 30.0).bfloat16()
+    else:
+        v = (v.float() * torch.tensor([1e-20, 1.0, 1e20, 1e5]).repeat_interleave(32)).bfloat16()
+    c = KVCache(B, L, h_kv, d, d, fmt="int4", page_size=64, device=DEV)
+    kk, vv = (x.to(DEV).expand(L, h_kv, d).contiguous() for x in (k, v))
+    for b in range(B):
+        c.append(kk, vv, i32([L] * B), cu_seqlens=i32([0] * (b + 1) + [L] * (B - b)))
+    q = bf((1, 1, h_kv, d), g).to(DEV).expand(B, 1, h_kv, d).contiguous()
+    out = c.attend(q, i32([L] * B), L)
+    assert c.device_status() == 0
+    unit = co.quantise(v.unflatten(-1, (-1, 32)))[1].double().repeat_interleave(32, -1) * 8
+    held = [tuple(x.expand(L, h_kv, d) for x in (co.through_4_bits(k), co.through_4_bits(v), unit))]
+    for b in (0, 37, B - 1):
+        check_attention(out[b:b + 1], None, q[b:b + 1], held, [L])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
 def test_attention_bound_above_lengths_and_repeats(fmt):
     """max_seqlen is only a bound, and the same call gives the same bits, workspace dirty or not."""
     lens = [900, 33, 0, 412]
