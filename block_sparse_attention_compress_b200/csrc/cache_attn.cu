@@ -17,7 +17,7 @@
 // MMA would take the nibbles as they are too, but on sm_100 it is carried out as conversions and
 // 16-bit MMAs: 781 us instead of TIME for 32 sequences of 64K tokens.)  A group's (s, z) come in behind
 // the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as one more MMA with
-// the stored pairs as A and the groups' query sums (two bf16 terms, 2^-18) as B.
+// the stored pairs as A and the groups' query sums (three bf16 terms: 24 bits) as B.
 //
 // Values in 4 bits: the same pairs of subnormals, by two tokens of a dim.  A token's weight is P s 2^k in f16 (one rounding, 2^-11),
 // k by group from the largest s met so far, so that weights stay below 2^15; weights below 2^-40 of
@@ -266,14 +266,14 @@ struct Walk {
 
 // Shared memory of a block: a ring (and later the joined rows) per warp, then in 4 bits the queries of
 // each row group: per tile of 8 rows the B fragments [DK / 32][32 lanes] x 16 bytes, the group sums'
-// [32 lanes] x 16 bytes and the rows' factors.
+// [32 lanes] x (16 + 8) bytes and the rows' factors.
 template <bool INT4, int DK, int DV, int NT, int U, int S>
 constexpr int warp_smem() {
   return std::max(S * U * Stage<INT4, DK, DV>::kBytes, NT * 8 * (DV + 4 + 2) * 4);
 }
 template <bool INT4, int DK, int NT>
 constexpr int query_smem() {
-  return INT4 ? NT * ((DK / 32 + 1) * 512 + 8 * 4) : 0;
+  return INT4 ? NT * ((DK / 32 + 1) * 512 + 256 + 8 * 4) : 0;
 }
 
 template <bool INT4, int DK, int DV, int NT, int W, int MINB, int U, int S, bool EXT>
@@ -294,7 +294,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   char* ring = smem + warp * kWarpBytes;
   const uint32_t ring_u = smem_u32(ring);
   char* sq = smem + W * kWarpBytes + rg * kQ;                     // this row group's queries
-  float* sq_sc = reinterpret_cast<float*>(sq + NT * (NG + 1) * 512);
+  char* sq_last = sq + NT * (NG + 1) * 512;
+  float* sq_sc = reinterpret_cast<float*>(sq_last + NT * 256);
 
   // ---- which tiles are this block's: `left` of them from tile t of item (b, h, rt) on
   asm volatile("griddepcontrol.launch_dependents;");   // the join may start to be set up
@@ -527,11 +528,14 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         const float up = pow2(e2);
         uint4* frag = reinterpret_cast<uint4*>(sq) + nt * (NG + 1) * 32 + lane;
         uint32_t* sums = reinterpret_cast<uint32_t*>(frag + NG * 32);
-        // (-8 sum, sum) of the groups' queries, each in two terms: one MMA's K holds eight groups' first
-        // terms and a second one the rest, or both terms of up to four groups; zeros where there is no group
+        uint32_t* last = reinterpret_cast<uint32_t*>(sq_last + (nt * 32 + lane) * 8);
+        // (-8 sum, sum) of the groups' queries, each in three terms.  An MMA's K holds eight pairs: a term of
+        // up to eight groups (words 2 i, 2 i + 1: term i of groups q4, q4 + 4), or two terms of up to four
+        // (word i: term i); zeros where there is no group
         if (ts == 0) {
-          if (NG < 4 && q4 >= NG) sums[0] = sums[1] = 0u;
-          if (NG > 4 && q4 + 4 >= NG) sums[1] = sums[3] = 0u;
+          if (NG <= 4) sums[3] = 0u;
+          if (NG < 4 && q4 >= NG) sums[0] = sums[1] = sums[2] = 0u;
+          if (NG > 4 && q4 + 4 >= NG) sums[1] = sums[3] = last[1] = 0u;
           // a query that is not finite makes its row NaN
           if (q4 == 0) sq_sc[nt * 8 + g8] = top >= 0x7f80u ? NAN : fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f);
         }
@@ -551,10 +555,12 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
                                      pack_f16(x[3] * 0.0625f, x[7] * 0.0625f));
           sum = warp_sum4(sum) * 0x1p-24f;   // the products carry 2^-24: so do the sums beside them
           if (gr % 4 == q4) {
-            const float first = __bfloat162float(__float2bfloat16_rn(sum)), rest = sum - first;
-            const uint32_t t0 = pack_bf16(-8.f * first, first), t1 = pack_bf16(-8.f * rest, rest);
-            sums[gr / 4] = t0;
-            sums[NG <= 4 ? 1 : 2 + gr / 4] = t1;
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              const float x = __bfloat162float(__float2bfloat16_rn(sum));
+              sum -= x;
+              (NG > 4 && term == 2 ? last : sums + (NG <= 4 ? term : 2 * term))[gr / 4] = pack_bf16(-8.f * x, x);
+            }
           }
         }
       }
@@ -613,8 +619,12 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       float s[U][NT][4];
       if constexpr (INT4) {
         uint4 q[NT];
+        uint2 qlast[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) q[nt] = *reinterpret_cast<const uint4*>(sq + (nt * (NG + 1) + NG) * 512 + lane * 16);
+        for (int nt = 0; nt < NT; ++nt) {
+          q[nt] = *reinterpret_cast<const uint4*>(sq + (nt * (NG + 1) + NG) * 512 + lane * 16);
+          if constexpr (NG > 4) qlast[nt] = *reinterpret_cast<const uint2*>(sq_last + (nt * 32 + lane) * 8);
+        }
 #pragma unroll
         for (int x = 0; x < U; ++x) {
           uint32_t kz[4];
@@ -628,7 +638,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_bf16_first(s[x][nt], kz[0], kz[1], kz[2], kz[3], q[nt].x, q[nt].y);
-            if constexpr (NG > 4) mma_bf16(s[x][nt], kz[0], kz[1], kz[2], kz[3], q[nt].z, q[nt].w);
+            mma_bf16(s[x][nt], kz[0], kz[1], kz[2], kz[3], q[nt].z, q[nt].w);
+            if constexpr (NG > 4) mma_bf16(s[x][nt], kz[0], kz[1], kz[2], kz[3], qlast[nt].x, qlast[nt].y);
           }
         }
         constexpr int GC = NG == 4 ? 4 : 2;   // groups whose words a lane loads at once
