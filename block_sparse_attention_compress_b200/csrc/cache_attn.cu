@@ -78,13 +78,20 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// (x, y) += (a, b) * f and (x, y) * f, as one packed instruction each
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float f) {
-  const float2 r = f2_unpack(f2_fma(f2_pack(a, b), f2_pack(f, f), f2_pack(x, y)));
-  x = r.x;
-  y = r.y;
+// (x, y) += (a, b) * f and (x, y) * f for a lane's J columns: two as one packed instruction
+template <int J>
+__device__ __forceinline__ void fma_columns(float& x, float& y, float a, float b, float f) {
+  if constexpr (J == 1) {
+    x = fmaf(a, f, x);
+  } else {
+    const float2 r = f2_unpack(f2_fma(f2_pack(a, b), f2_pack(f, f), f2_pack(x, y)));
+    x = r.x;
+    y = r.y;
+  }
 }
-__device__ __forceinline__ float2 mul2(float a, float b, float f) {
+template <int J>
+__device__ __forceinline__ float2 mul_columns(float a, float b, float f) {
+  if constexpr (J == 1) return make_float2(a * f, 0.f);
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_pack(a, b)), "l"(f2_pack(f, f)));
   return f2_unpack(d);
@@ -144,7 +151,7 @@ struct Plan {
   int blocks, min_tiles, row_groups;
   int per_g;                  // r / G = r per_g >> 16 for the rows r < 256 of a call
   int first[4], last[4];      // of each row tile: the first and the last new token it has rows of
-  bool whole, nt2;
+  bool whole;
 };
 __device__ __forceinline__ int row_token(const Plan& p, int r) { return r * p.per_g >> 16; }
 
@@ -276,13 +283,15 @@ constexpr int query_smem() {
   return INT4 ? NT * ((DK / 32 + 1) * 512 + 256 + 8 * 4) : 0;
 }
 
-template <bool INT4, int DK, int DV, int NT, int W, int MINB, int U, int S, bool EXT>
+template <bool INT4, int DK, int DV, int NT, int J, int W, int MINB, int U, int S, bool EXT>
 __global__ void __launch_bounds__(W * 32, MINB)
 cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* __restrict__ cuts, float2* __restrict__ part_ml,
                   float* __restrict__ part_o) {
   using T = Stage<INT4, DK, DV>;
   constexpr int NG = DK / 32, NH = DV / 32, MT = DV / 16, KS = DK / 16;
-  constexpr int kCols = NT * 8, kRow = DV + 4;
+  // a warp's rows: J of a lane's two columns hold one
+  constexpr int kCols = NT * 4 * J, kRow = DV + 4;
+  const auto row_of = [](int nt, int column) { return J == 2 ? nt * 8 + column : column >> 1; };
   constexpr int kWarpBytes = warp_smem<INT4, DK, DV, NT, U, S>(), kStep = kTile * U, kQ = query_smem<INT4, DK, NT>();
   extern __shared__ __align__(128) char smem[];
   __shared__ long long s_scan[W];
@@ -496,12 +505,12 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 
     // ---- queries as B fragments: row n = lane / 4 of each tile of 8.  4 bits: through shared memory
     uint32_t qf[INT4 ? 1 : NT][INT4 ? 1 : KS][2];
-    float sc[NT][2];                    // what a column's raw score is multiplied by (natural units)
-    int pos[NT][2];                     // the columns' positions
-    float slope[EXT ? NT : 1][2];
+    float sc[NT][J];                    // what a column's raw score is multiplied by (natural units)
+    int pos[NT][J];                     // the columns' positions
+    float slope[EXT ? NT : 1][J];
 #pragma unroll(INT4 ? 1 : NT)
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = min(r0 + nt * 8 + g8, R - 1), i = row_token(pl, r), g = r - i * a.G;
+      const int r = min(r0 + row_of(nt, g8), R - 1), i = row_token(pl, r), g = r - i * a.G;
       const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
       if constexpr (!INT4) {
 #pragma unroll
@@ -569,8 +578,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int rc = min(r0 + nt * 8 + 2 * q4 + j, R - 1), ic = row_token(pl, rc);
+      for (int j = 0; j < J; ++j) {
+        const int rc = min(r0 + row_of(nt, 2 * q4 + j), R - 1), ic = row_token(pl, rc);
         sc[nt][j] = INT4 ? sq_sc[nt * 8 + 2 * q4 + j] : a.scale;
         pos[nt][j] = sp.p0 + ic;
         if constexpr (EXT) slope[nt][j] = a.slopes ? __ldg(a.slopes + h * a.G + rc - ic * a.G) * kLog2e : 0.f;
@@ -578,13 +587,13 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       }
 
     float o[MT][NT][4];
-    float m[NT][2], l[NT][2], zacc[INT4 ? NT : 1][NH][2];
+    float m[NT][J], l[NT][J], zacc[INT4 ? NT : 1][NH][J];
     float top_s[INT4 ? NH : 1];   // 2^k of each group's weights
     uint32_t max_s[INT4 ? NH : 1];   // the largest s that k allows, as bf16 bits
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < J; ++j) {
         m[nt][j] = kNone;
         l[nt][j] = 0.f;
         if constexpr (INT4) {
@@ -668,8 +677,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma_f16(acc[nt], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q[nt].z, q[nt].w);
-                fma2(s[x][nt][0], s[x][nt][1], acc[nt][0], acc[nt][1], s0);
-                fma2(s[x][nt][2], s[x][nt][3], acc[nt][2], acc[nt][3], s1);
+                fma_columns<J>(s[x][nt][0], s[x][nt][1], acc[nt][0], acc[nt][1], s0);
+                fma_columns<J>(s[x][nt][2], s[x][nt][3], acc[nt][2], acc[nt][3], s1);
               }
             }
           }
@@ -704,7 +713,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; e += 3 - J) {
             float y = s[x][nt][e] * sc[nt][e & 1];
             if constexpr (EXT) {
               if (a.softcap > 0.f) y = capped(y, a.softcap, a.inv_softcap);
@@ -718,16 +727,16 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 4; e += 3 - J) {
               const int u = u0 + x * kTile + g8 + 8 * (e >> 1), p = pos[nt][e & 1];
               if ((gone >> x & 1) || u > p || u < sp.lo || (a.window > 0 && u <= p - a.window)) s[x][nt][e] = -INFINITY;
             }
       }
-      float top[NT][2];
+      float top[NT][J];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < J; ++j) {
           top[nt][j] = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
 #pragma unroll
           for (int x = 1; x < U; ++x) top[nt][j] = fmaxf(top[nt][j], fmaxf(s[x][nt][j], s[x][nt][j + 2]));
@@ -752,7 +761,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int j = 0; j < J; ++j) {
             float x = top[nt][j];
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -777,7 +786,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; e += 3 - J) {
             const float p = ex2(s[x][nt][e] - m[nt][e & 1]);
             s[x][nt][e] = p;
             l[nt][e & 1] += p;
@@ -805,11 +814,11 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&p)[4] = s[x][nt];
-              const float2 w0 = mul2(p[0], p[1], s0), w1 = mul2(p[2], p[3], s1);
+              const float2 w0 = mul_columns<J>(p[0], p[1], s0), w1 = mul_columns<J>(p[2], p[3], s1);
               pb[nt][0] = movmatrix(pack_f16(w0.x, w0.y));
               pb[nt][1] = movmatrix(pack_f16(w1.x, w1.y));
-              fma2(zacc[nt][gr][0], zacc[nt][gr][1], p[0], p[1], z0);
-              fma2(zacc[nt][gr][0], zacc[nt][gr][1], p[2], p[3], z1);
+              fma_columns<J>(zacc[nt][gr][0], zacc[nt][gr][J - 1], p[0], p[1], z0);
+              fma_columns<J>(zacc[nt][gr][0], zacc[nt][gr][J - 1], p[2], p[3], z1);
             }
             const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
             const uint32_t lo = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel), lo8 = lo >> 8;
@@ -829,7 +838,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int j = 0; j < J; ++j) {
                 float z = zacc[nt][gr][j];
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
@@ -888,8 +897,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int col = nt * 8 + 2 * q4 + j;
+      for (int j = 0; j < J; ++j) {
+        const int col = row_of(nt, 2 * q4 + j);
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], d);
         if (g8 == 0) {
@@ -1025,22 +1034,28 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
 }
 
 // Warps per block, blocks per SM, tiles of 16 tokens per step.
-template <bool INT4, int NT>
+template <bool INT4, int NT, int J>
 struct Shape {
+  static constexpr bool kInt4 = INT4;
+  static constexpr int kNT = NT, kJ = J, kRows = NT * 4 * J;
   static constexpr int W = INT4 ? 4 : 8;
-  static constexpr int B = INT4 ? (NT == 2 ? 2 : 4) : 1;
+  static constexpr int B = INT4 ? (NT == 2 ? 2 : 3) : 1;
   static constexpr int U = INT4 ? 2 : 1;
 };
 // Stages of the ring: as many as fit beside the other blocks of the SM, at most 4 (4 bits: 3).
-template <bool INT4, int DK, int DV, int NT>
+template <bool INT4, int DK, int DV, int NT, int J>
 constexpr int stages() {
-  using H = Shape<INT4, NT>;
+  using H = Shape<INT4, NT, J>;
   constexpr int room = 227 * 1024 / H::B - 1024 - 1024 - query_smem<INT4, DK, NT>();
   return std::min(INT4 ? 3 : 4, room / (H::W * H::U * Stage<INT4, DK, DV>::kBytes));
 }
+// f of the shape a call's rows take: up to 16 of a head, its queries times its new tokens.  Four at most
+// use one of a lane's columns (4 bits, 32 heads of one query over 64K tokens: 86 us instead of 97); a bf16
+// cache waits for memory either way.
 template <class F>
-auto with_shape(bool int4, bool nt2, F f) {
-  return int4 ? (nt2 ? f(Shape<true, 2>()) : f(Shape<true, 1>())) : nt2 ? f(Shape<false, 2>()) : f(Shape<false, 1>());
+auto with_shape(bool int4, int rows, F f) {
+  if (!int4) return rows > 8 ? f(Shape<false, 2, 2>()) : f(Shape<false, 1, 2>());
+  return rows > 8 ? f(Shape<true, 2, 2>()) : rows > 4 ? f(Shape<true, 1, 2>()) : f(Shape<true, 1, 1>());
 }
 
 constexpr int kSms = 148;
@@ -1050,11 +1065,10 @@ constexpr int kWholeTokens = 128;
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   Plan p;
   const int R = a.n_new * a.G;
-  p.nt2 = R > 8;
-  int W = 0, step = 0, resident = 0;
-  with_shape(c.int4, p.nt2, [&](auto h) { W = h.W; step = kTile * h.U; resident = h.B; });
+  int W = 0, step = 0, resident = 0, rows = 0;
+  with_shape(c.int4, R, [&](auto h) { W = h.W; step = kTile * h.U; resident = h.B; rows = h.kRows; });
   p.row_groups = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-  p.tile_rows = (p.nt2 ? 16 : 8) * p.row_groups;
+  p.tile_rows = rows * p.row_groups;
   p.row_tiles = (R + p.tile_rows - 1) / p.tile_rows;
   p.per_g = (65536 + a.G - 1) / a.G;
   for (int rt = 0; rt < p.row_tiles; ++rt) {   // R <= 256: at most four tiles, of 64 rows
@@ -1102,15 +1116,14 @@ cudaError_t launch_join(const CacheArgs& c, const CacheAttnArgs& a, const Plan& 
   return cudaLaunchKernelEx(&cfg, cache_join_kernel<DV, WPR>, c, a, p, cuts, ml, o);
 }
 
-template <bool INT4, int DK, int DV, int NT, bool EXT>
+template <class H, bool INT4, int DK, int DV, bool EXT>
 cudaError_t launch_variant(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, cudaStream_t st) {
-  using H = Shape<INT4, NT>;
-  constexpr int S = stages<INT4, DK, DV, NT>();
+  constexpr int NT = H::kNT, J = H::kJ, S = stages<INT4, DK, DV, NT, J>();
   constexpr int kRing = H::W * warp_smem<INT4, DK, DV, NT, H::U, S>(), kQ = query_smem<INT4, DK, NT>();
   static_assert(S >= 2 && (kRing + kQ + 2048) * H::B <= 228 * 1024, "the rings of the resident blocks fit an SM");
   static_assert(kRing + 4 * kQ <= 227 * 1024, "a block's shared memory");
   static PerDevice set;
-  auto* f = cache_attn_kernel<INT4, DK, DV, NT, H::W, H::B, H::U, S, EXT>;
+  auto* f = cache_attn_kernel<INT4, DK, DV, NT, J, H::W, H::B, H::U, S, EXT>;
   cudaError_t e = set.once([&] { return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 4 * kQ); });
   if (e != cudaSuccess) return e;
   const Parts x = parts_of(c, p);
@@ -1131,13 +1144,10 @@ template <int DK, int DV>
 cudaError_t launch_dims(const CacheArgs& c, const CacheAttnArgs& a, cudaStream_t st) {
   const Plan p = plan_of(c, a);
   const bool ext = a.softcap > 0.f || a.slopes;
-#define NSA_VARIANT(I, N, X) launch_variant<I, DK, DV, N, X>(c, a, p, st)
-  if (c.int4)
-    return p.nt2 ? (ext ? NSA_VARIANT(true, 2, true) : NSA_VARIANT(true, 2, false))
-                 : (ext ? NSA_VARIANT(true, 1, true) : NSA_VARIANT(true, 1, false));
-  return p.nt2 ? (ext ? NSA_VARIANT(false, 2, true) : NSA_VARIANT(false, 2, false))
-               : (ext ? NSA_VARIANT(false, 1, true) : NSA_VARIANT(false, 1, false));
-#undef NSA_VARIANT
+  return with_shape(c.int4, a.n_new * a.G, [&](auto h) {
+    using H = decltype(h);
+    return ext ? launch_variant<H, H::kInt4, DK, DV, true>(c, a, p, st) : launch_variant<H, H::kInt4, DK, DV, false>(c, a, p, st);
+  });
 }
 
 }  // namespace
