@@ -24,27 +24,15 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Dims d0 .. d0 + 7 of a head at `head`, rotated by the table row cs (cosines, then sines):
-// (a, b) -> (a cos - b sin, b cos + a sin).  Products and sums are rounded one by one (no
+// Dims d0 .. d0 + 7 of a head at `head`, the pairs (j, j + rot / 2) rotated by the table row cs (cosines,
+// then sines): (a, b) -> (a cos - b sin, b cos + a sin).  Products and sums are rounded one by one (no
 // contraction), so that the result is the same wherever it is computed.
-__device__ __forceinline__ uint4 rotated_chunk(const __nv_bfloat16* head, int d0, const float* cs, int rot,
-                                               int interleaved) {
+__device__ __forceinline__ uint4 rotated_chunk(const __nv_bfloat16* head, int d0, const float* cs, int rot) {
   const uint4 own = __ldg(reinterpret_cast<const uint4*>(head + d0));
-  if (cs == nullptr || d0 >= rot) return own;
+  if (d0 >= rot) return own;
   const int half = rot >> 1;
   float x[8], y[8];
   unpack8(own, x);
-  if (interleaved) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (d0 >> 1)));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + (d0 >> 1)));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], cc[i]), __fmul_rn(x[2 * i + 1], ss[i]));
-      y[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], cc[i]), __fmul_rn(x[2 * i], ss[i]));
-    }
-    return pack8(y);
-  }
   const bool first = d0 < half;   // which member of its pairs this chunk holds
   const int j = first ? d0 : d0 - half;
   float o[8];
@@ -310,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheArgs c, 
       const size_t i = (size_t)i0 + tok[f];
       if (INT4 && y[f] < nk)
         v[f] = rotated_chunk(static_cast<const __nv_bfloat16*>(a.k) + i * a.k_stride + y[f] / (DK / 8) * DK, y[f] % (DK / 8) * 8,
-                             a.cos_sin ? a.cos_sin + (size_t)s_place[tok[f]].pos * a.rot : nullptr, a.rot, a.interleaved);
+                             a.cos_sin + (size_t)s_place[tok[f]].pos * rot, rot);   // by_chunk: there is a table
       else
         v[f] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + i * a.v_stride) + (y[f] - nk));
     }

@@ -9,27 +9,34 @@
 //                             P^T's B fragment by movmatrix.
 // The operands come from registers (warp-level MMA): in 4 bits a tcgen05 form would have to write
 // every widened value to shared memory and read it back, 640 bytes a token against the 200 that
-// are stored, which alone takes longer than the cache's bytes.
+// are stored, about 210 cycles of an SM's shared memory for 16 tokens of (192, 128); HBM takes 120.
 //
 // Keys in 4 bits: w & 0x000f000f and w & 0x00f000f0 are pairs of f16 subnormals c 2^-24 and
 // c 2^-20, which the tensor cores multiply exactly: no conversion.  The queries of the latter are
 // divided by 16, and every query row is scaled by a power of two so that f16 holds it.  (The e4m3
 // MMA would take the nibbles as they are too, but on sm_100 it is carried out as conversions and
-// 16-bit MMAs: 781 us instead of TIME for 32 sequences of 64K tokens.)  A group's (s, z) come in behind
-// the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as one more MMA with
+// 16-bit MMAs: 781 us instead of 571 for 32 sequences of 64K tokens.)  A group's (s, z) come in behind
+// the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as more MMAs with
 // the stored pairs as A and the groups' query sums (three bf16 terms: 24 bits) as B.
 //
-// Values in 4 bits: the same pairs of subnormals, by two tokens of a dim.  A token's weight is P s 2^k in f16 (one rounding, 2^-11),
-// k by group from the largest s met so far, so that weights stay below 2^15; weights below 2^-40 of
-// that limit vanish.  P (z - 8 s) is summed in fp32.  The tensor cores cut off sums instead
-// of rounding them (measured: 4096 steps lose 2e-4), so every 32 tiles the offset's sum is taken into
-// the accumulators, which leaves them at the size of the result.
+// Values in 4 bits: the same pairs of subnormals, by two tokens of a dim.  A token's weight is
+// P s 2^k in f16 (one rounding, 2^-11), k by group from the largest s met so far, so that weights
+// stay below 2^15: full digits down to scales 2^-20 of the largest, nothing below 2^-30 of it.  P (z - 8 s)
+// is summed in fp32.  The tensor cores cut off sums instead of rounding them (measured: 4096 steps
+// lose 2e-4), so every 32 tiles the offset's sum is taken into the accumulators, which leaves them at
+// the size of the result.
 //
 // Every warp copies its own tiles of 16 tokens into a ring in shared memory (cp.async, no block-wide
 // waits).  The tiles of all sequences and heads are laid end to end and cut into equal runs, one
 // per block, so unequal lengths and head counts fill the GPU alike; a sequence cut into several runs
 // leaves a part in each block's slots and a second small kernel joins the parts by their maxima and
 // sums, in a fixed order.
+//
+// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 222 us, 6.0 TB/s.  32 x 64K tokens
+// in 4 bits, same heads: 490 us, 3.4 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 155 us, 4.3
+// TB/s.  In 4 bits the issue slots bound it, not HBM: about 540 instructions a tile of 16 tokens and 16 rows, of
+// which 108 unpack nibbles, at 2 a cycle and SM; logic at half rate, MMAs and fp32 products compete for
+// the same slots (4 MMAs, 16 logic and 16 fma instructions take 58 cycles, not 32).
 #include <algorithm>
 
 #include "cache.cuh"
