@@ -367,6 +367,35 @@ def test_attention_caps_and_slopes(fmt, cap, steep, scale):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_options_at_the_ends_of_their_ranges(fmt):
+    """Windows that reach everything are none; caps far above the scores change nothing, far below make them equal."""
+    lens = [130, 20, 3, 0]
+    c, q, held, out, lse, _ = run_attention(fmt, 64, 64, 16, 2, 2, lens, 5, seed=40)
+    check_attention(out, lse, q, held, lens)
+    for window in (130, 131, 2 ** 31 - 1):
+        assert torch.equal(c.attend(q, i32(lens), 130, window=window), out)
+    for cap in (1e32, 3e38):
+        assert torch.equal(c.attend(q, i32(lens), 130, softcap=cap), out)
+    for cap in (1e-30, 1e-44):
+        flat = c.attend(q, i32(lens), 130, softcap=cap)
+        check_attention(flat, None, torch.zeros_like(q), held, lens)
+    check_attention(c.attend(q, i32(lens), 130, softcap=1e20), None, q, held, lens)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("odd", [math.nan, math.inf])
+def test_a_query_that_is_not_finite_spoils_its_row_alone(fmt, odd):
+    lens = [700, 40]
+    c, q, _, out, _, _ = run_attention(fmt, 128, 128, 16, 2, 4, lens, 3, seed=41)
+    q[0, 1, 3, 17] = odd
+    again = c.attend(q, i32(lens), 700)
+    assert torch.isnan(again[0, 1, 3].float()).all()
+    same = torch.ones(out.shape[:3], dtype=torch.bool)
+    same[0, 1, 3] = False
+    assert torch.equal(again[same.to(DEV)], out[same.to(DEV)])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
 @pytest.mark.parametrize("ks,vs,qs", [(1e-4, 1e3, 1.0), (30.0, 1.0, 1.0), (1.0, 1e-20, 1e3), (1e10, 1e20, 1e-10), (1.0, 1.0, 0.0)])
 def test_attention_magnitudes(fmt, ks, vs, qs):
     """Small, large and lopsided inputs: weights from flat to one token taking all."""
