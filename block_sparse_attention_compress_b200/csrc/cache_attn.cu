@@ -158,7 +158,7 @@ struct Plan {
   int blocks, min_tiles, row_groups;
   int per_g;                  // r / G = r per_g >> 16 for the rows r < 256 of a call
   int first[4], last[4];      // of each row tile: the first and the last new token it has rows of
-  bool whole;
+  bool whole, small;          // small: the tiles of all items count in 32 bits
 };
 __device__ __forceinline__ int row_token(const Plan& p, int r) { return r * p.per_g >> 16; }
 
@@ -181,9 +181,9 @@ __device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs&
   s.tiles = max(1, (s.hi - s.base + STEP - 1) / STEP);
   return s;
 }
-// a / b; 64-bit division is a hundred instructions
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+// a / b for counts: 64-bit division is a hundred instructions
+__device__ __forceinline__ int runs_before(long long a, long long b) {
+  return ((a | b) >> 31) == 0 ? (int)((uint32_t)a / (uint32_t)b) : (int)(a / b);
 }
 
 __device__ __forceinline__ void check_length(const CacheArgs& c, const CacheAttnArgs& a, int b) {
@@ -301,7 +301,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   const auto row_of = [](int nt, int column) { return J == 2 ? nt * 8 + column : column >> 1; };
   constexpr int kWarpBytes = warp_smem<INT4, DK, DV, NT, U, S>(), kStep = kTile * U, kQ = query_smem<INT4, DK, NT>();
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long s_scan[W];
+  __shared__ long long s_scan[2][W];
   __shared__ long long s_off;
   __shared__ int s_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, q4 = lane & 3;
@@ -328,85 +328,92 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     left = (long long)span_of<kStep>(c, a, pl, b, rt).tiles + extra;
     if (h == 0 && rt == 0 && threadIdx.x == 0) check_length(c, a, b);
   } else {
-    // An item's share of the work: its tiles and, before them, what its start costs in tiles (unit 0); or
-    // its runs of `unit` tiles.  And that of a sequence's items.
-    const auto units = [&](int bb, int x, long long unit) {
-      const int n = span_of<kStep>(c, a, pl, bb, x).tiles;
-      return unit == 0 ? n + extra : (int)quotient(n + unit - 1, unit);
-    };
-    const auto weight = [&](int bb, long long unit) {
-      long long w = 0;
-      for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x, unit);
-      return w * c.h_kv;
-    };
-    const int strip = (c.batch + W * 32 - 1) / (W * 32);
-    const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
-    // the strips' sums: of those before this thread's, and of all
-    const auto scan = [&](long long mine, long long& total) {
-      long long upto = mine;
+    const auto cut_work = [&](auto zero) {   // false: nothing is left for this block
+      using N = decltype(zero);              // 32 bits wherever the count of tiles allows it
+      const auto quotient = [](N x, N y) { return sizeof(N) == 4 ? (N)((uint32_t)x / (uint32_t)y) : (N)(x / y); };
+      // An item's share of the work: its tiles and, before them, what its start costs in tiles (unit 0); or
+      // its runs of `unit` tiles.  And that of a sequence's items.
+      const auto units = [&](int bb, int x, N unit) -> N {
+        const int n = span_of<kStep>(c, a, pl, bb, x).tiles;
+        return unit == 0 ? n + extra : quotient(n + unit - 1, unit);
+      };
+      const auto weight = [&](int bb, N unit) {
+        N w = 0;
+        for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x, unit);
+        return w * c.h_kv;
+      };
+      const int strip = (c.batch + W * 32 - 1) / (W * 32);
+      const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
+      // the strips' sums: of those before this thread's, and of all
+      const auto scan = [&](N mine, N& total, long long* warps) {
+        N upto = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += y;
-      }
-      if (lane == 31) s_scan[warp] = upto;
-      __syncthreads();
-      total = 0;
+        for (int d = 1; d < 32; d <<= 1) {
+          const N y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += y;
+        }
+        if (lane == 31) warps[warp] = upto;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w < warp) upto += s_scan[w];
-        total += s_scan[w];
+        for (int w = 0; w < W; ++w) {
+          const N y = (N)warps[w];
+          if (w < warp) upto += y;
+          total += y;
+        }
+        return (N)(upto - mine);
+      };
+      N mine = 0, total;
+      for (int x = b0; x < b1; ++x) {
+        mine += weight(x, 0);
+        if (blockIdx.x == 0) check_length(c, a, x);
+      }
+      N before = scan(mine, total, s_scan[0]), run = max((N)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
+      // Runs that end with their item spare a block the end of one item and the start of the next (about 5 us),
+      // but are longer, since items end inside their last run.  While a run is short, that is the cheaper
+      // cut (64 items of 1100 tokens 15.6 us instead of 18.6); long runs hide those behind the SM's other
+      // blocks, and for a few items finding the runs costs more.
+      const N items = (N)c.batch * c.h_kv * pl.row_tiles, spare = (N)gridDim.x - items;
+      if (spare > 0 && items >= 16 && run <= kShort * streams) {
+        const N longer = max((N)pl.min_tiles, quotient(total + spare - 1, spare));
+        whole_runs = longer <= kShort * streams && longer - run <= kLonger * streams;
+        if (whole_runs) {
+          run = longer;
+          mine = 0;
+          for (int x = b0; x < b1; ++x) mine += weight(x, run);
+          before = scan(mine, total, s_scan[1]);   // in runs: sum over items of ceil(tiles / run) <= spare + items
+        }
+      }
+      const N pos = whole_runs ? (N)blockIdx.x : run * (N)blockIdx.x, unit = whole_runs ? run : 0;
+      if (pos >= total) return false;
+      if (before <= pos && pos < before + mine) {
+        N off = pos - before;
+        int x = b0;
+        for (N w; off >= (w = weight(x, unit)); ++x) off -= w;
+        s_b = x;
+        s_off = off;
       }
       __syncthreads();
-      return upto - mine;
-    };
-    long long mine = 0, total;
-    for (int x = b0; x < b1; ++x) {
-      mine += weight(x, 0);
-      if (blockIdx.x == 0) check_length(c, a, x);
-    }
-    long long before = scan(mine, total);
-    per = max((long long)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
-    // Runs that end with their item spare a block the end of one item and the start of the next (about 5 us),
-    // but are longer, since items end inside their last run.  While a run is short, that is the cheaper
-    // cut (64 items of 1100 tokens 15.6 us instead of 18.6); long runs hide those behind the SM's other
-    // blocks, and for a few items finding the runs costs more.
-    const long long items = (long long)c.batch * c.h_kv * pl.row_tiles, spare = gridDim.x - items;
-    if (spare > 0 && items >= 16) {
-      const long long longer = max((long long)pl.min_tiles, quotient(total + spare - 1, spare));
-      whole_runs = longer <= kShort * streams && longer - per <= kLonger * streams;
+      b = s_b;
+      N head = 0;   // units of a head, in all row tiles
+      for (int x = 0; x < pl.row_tiles; ++x) head += units(b, x, unit);
+      h = (int)quotient((N)s_off, head);
+      N at = (N)s_off - (N)h * head;
+      rt = 0;
+      for (N n; at >= (n = units(b, rt, unit)); ++rt) at -= n;
+      t = (int)at;
+      left = min(run, (N)(total - pos));
       if (whole_runs) {
-        per = longer;
-        mine = 0;
-        for (int x = b0; x < b1; ++x) mine += weight(x, per);
-        before = scan(mine, total);   // in runs: sum over items of ceil(tiles / per) <= spare + items
+        t = t * (int)run + extra;
+        left = min(run, (N)(span_of<kStep>(c, a, pl, b, rt).tiles + extra - t));
       }
-    }
-    pos0 = whole_runs ? blockIdx.x : per * blockIdx.x;
-    if (pos0 >= total) {
+      pos0 = pos;
+      per = run;
+      return true;
+    };
+    if (!(pl.small ? cut_work(0) : cut_work(0ll))) {
       if (threadIdx.x == 0) cuts[blockIdx.x] = Cut{0, 0, -1, 0};
       return;
-    }
-    const long long unit = whole_runs ? per : 0;
-    if (before <= pos0 && pos0 < before + mine) {
-      long long off = pos0 - before;
-      int x = b0;
-      for (long long w; off >= (w = weight(x, unit)); ++x) off -= w;
-      s_b = x;
-      s_off = off;
-    }
-    __syncthreads();
-    b = s_b;
-    int head = 0;   // units of a head, in all row tiles
-    for (int x = 0; x < pl.row_tiles; ++x) head += units(b, x, unit);
-    h = (int)quotient(s_off, head);
-    t = (int)(s_off - (long long)h * head);
-    rt = 0;
-    for (int n; t >= (n = units(b, rt, unit)); ++rt) t -= n;
-    left = min(per, total - pos0);
-    if (whole_runs) {
-      t = t * (int)per + extra;
-      left = min(per, (long long)span_of<kStep>(c, a, pl, b, rt).tiles + extra - t);
     }
   }
 
@@ -447,8 +454,18 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     if (first == 0 && take < sp.tiles) {
       cut.b = b;
       cut.head_tile = h * pl.row_tiles + rt;
-      cut.last = (int)(whole_runs ? blockIdx.x + quotient(sp.tiles - 1, per) : quotient(pos0 - t + extra + sp.tiles - 1, per));
+      cut.last = whole_runs ? (int)blockIdx.x + runs_before(sp.tiles - 1, per) : runs_before(pos0 - t + extra + sp.tiles - 1, per);
       cut.rows = tile_rows;
+    }
+
+    // ---- queries on their way: row n = lane / 4 of each tile of 8
+    uint4 qraw[NT][NG];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = min(r0 + row_of(nt, g8), R - 1), i = row_token(pl, r), g = r - i * a.G;
+      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
+#pragma unroll
+      for (int gr = 0; gr < NG; ++gr) qraw[nt][gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
     }
 
     // ---- this warp's run of tiles, [ta, tb) of the item
@@ -515,23 +532,22 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     float sc[NT][J];                    // what a column's raw score is multiplied by (natural units)
     int pos[NT][J];                     // the columns' positions
     float slope[EXT ? NT : 1][J];
-#pragma unroll(INT4 ? 1 : NT)
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = min(r0 + row_of(nt, g8), R - 1), i = row_token(pl, r), g = r - i * a.G;
-      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.n_new + i) * a.h_q + h * a.G + g) * DK;
       if constexpr (!INT4) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2*>(qr + 32 * (ks >> 1) + 8 * q4 + 4 * (ks & 1)));
-          qf[nt][ks][0] = u.x;
-          qf[nt][ks][1] = u.y;
+        for (int gr = 0; gr < NG; ++gr) {
+          const uint4 u = qraw[nt][gr];
+          qf[nt][2 * gr][0] = u.x;
+          qf[nt][2 * gr][1] = u.y;
+          qf[nt][2 * gr + 1][0] = u.z;
+          qf[nt][2 * gr + 1][1] = u.w;
         }
       } else {
-        uint4 u[NG];
+        const uint4(&u)[NG] = qraw[nt];
         uint32_t top = 0;   // the largest |q| as bf16 bits, in both halves
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
-          u[gr] = __ldg(reinterpret_cast<const uint4*>(qr + 32 * gr + 8 * q4));
           const uint32_t w[4] = {u[gr].x, u[gr].y, u[gr].z, u[gr].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
@@ -939,10 +955,14 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       const char* base = smem + (rr / kCols) * kWarpBytes;   // the first warp of the row's group
       const size_t step = (size_t)pl.row_groups * kWarpBytes;
       float mm = kNone;
-      for (int w = 0; w < streams; ++w) mm = fmaxf(mm, reinterpret_cast<const float*>(base + w * step)[kCols * kRow + col]);
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (w < streams) mm = fmaxf(mm, reinterpret_cast<const float*>(base + w * step)[kCols * kRow + col]);
       float ll = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < streams; ++w) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (w >= streams) break;
         const float* f = reinterpret_cast<const float*>(base + w * step);
         const float lw = f[kCols * kRow + kCols + col], k = ex2(f[kCols * kRow + col] - mm);
         if (lw == 0.f) continue;
@@ -1087,6 +1107,7 @@ Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   if (a.window > 0) range = std::min<long long>(range, (long long)a.window + a.n_new + kTile);
   const long long tiles = (range + step - 1) / step, items = (long long)c.batch * c.h_kv * p.row_tiles;
   p.min_tiles = 2 * (W / p.row_groups);
+  p.small = items * (tiles + 4 * W) < (1 << 30);
   p.whole = range <= kWholeTokens * (W / p.row_groups) * (items >= 64 ? 2 : 1);
   const long long most = (long long)kSms * resident;
   // items <= 2^31 (cache_attn_fits), tiles <= 2^26
