@@ -303,7 +303,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   extern __shared__ __align__(128) char smem[];
   __shared__ long long s_scan[2][W];
   __shared__ long long s_off;
-  __shared__ int s_b;
+  __shared__ int s_b, s_h;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, q4 = lane & 3;
   const int rg = warp % pl.row_groups, streams = W / pl.row_groups, ts = warp / pl.row_groups;
   const int R = a.n_new * a.G;
@@ -331,19 +331,21 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     const auto cut_work = [&](auto zero) {   // false: nothing is left for this block
       using N = decltype(zero);              // 32 bits wherever the count of tiles allows it
       const auto quotient = [](N x, N y) { return sizeof(N) == 4 ? (N)((uint32_t)x / (uint32_t)y) : (N)(x / y); };
-      // An item's share of the work: its tiles and, before them, what its start costs in tiles (unit 0); or
-      // its runs of `unit` tiles.  And that of a sequence's items.
-      const auto units = [&](int bb, int x, N unit) -> N {
-        const int n = span_of<kStep>(c, a, pl, bb, x).tiles;
-        return unit == 0 ? n + extra : quotient(n + unit - 1, unit);
-      };
-      const auto weight = [&](int bb, N unit) {
-        N w = 0;
-        for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x, unit);
-        return w * c.h_kv;
-      };
       const int strip = (c.batch + W * 32 - 1) / (W * 32);
       const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
+      // a thread with one sequence of one row tile looks its length up once
+      const bool single = strip == 1 && pl.row_tiles == 1;
+      const int own = single && b0 < b1 ? span_of<kStep>(c, a, pl, b0, 0).tiles : 0;
+      // An item's share of the work: its tiles and, before them, what its start costs in tiles (unit 0); or
+      // its runs of `unit` tiles.  And that of a head, in all row tiles.
+      const auto share = [&](int n, N unit) -> N { return unit == 0 ? n + extra : quotient(n + unit - 1, unit); };
+      const auto units = [&](int bb, int x, N unit) { return share(span_of<kStep>(c, a, pl, bb, x).tiles, unit); };
+      const auto head_units = [&](int bb, N unit) {
+        if (single) return share(own, unit);
+        N w = 0;
+        for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x, unit);
+        return w;
+      };
       // the strips' sums: of those before this thread's, and of all
       const auto scan = [&](N mine, N& total, long long* warps) {
         N upto = mine;
@@ -365,7 +367,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       };
       N mine = 0, total;
       for (int x = b0; x < b1; ++x) {
-        mine += weight(x, 0);
+        mine += head_units(x, 0) * c.h_kv;
         if (blockIdx.x == 0) check_length(c, a, x);
       }
       N before = scan(mine, total, s_scan[0]), run = max((N)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
@@ -380,27 +382,28 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
         if (whole_runs) {
           run = longer;
           mine = 0;
-          for (int x = b0; x < b1; ++x) mine += weight(x, run);
+          for (int x = b0; x < b1; ++x) mine += head_units(x, run) * c.h_kv;
           before = scan(mine, total, s_scan[1]);   // in runs: sum over items of ceil(tiles / run) <= spare + items
         }
       }
       const N pos = whole_runs ? (N)blockIdx.x : run * (N)blockIdx.x, unit = whole_runs ? run : 0;
       if (pos >= total) return false;
       if (before <= pos && pos < before + mine) {
-        N off = pos - before;
+        N off = pos - before, head;
         int x = b0;
-        for (N w; off >= (w = weight(x, unit)); ++x) off -= w;
+        for (; off >= (head = head_units(x, unit)) * c.h_kv; ++x) off -= head * c.h_kv;
+        const N skip = quotient(off, head);
         s_b = x;
-        s_off = off;
+        s_h = (int)skip;
+        s_off = off - skip * head;
       }
       __syncthreads();
       b = s_b;
-      N head = 0;   // units of a head, in all row tiles
-      for (int x = 0; x < pl.row_tiles; ++x) head += units(b, x, unit);
-      h = (int)quotient((N)s_off, head);
-      N at = (N)s_off - (N)h * head;
+      h = s_h;
+      N at = (N)s_off;
       rt = 0;
-      for (N n; at >= (n = units(b, rt, unit)); ++rt) at -= n;
+      if (pl.row_tiles > 1)
+        for (N n; at >= (n = units(b, rt, unit)); ++rt) at -= n;
       t = (int)at;
       left = min(run, (N)(total - pos));
       if (whole_runs) {
