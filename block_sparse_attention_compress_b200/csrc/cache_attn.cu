@@ -1069,7 +1069,7 @@ struct Shape {
   static constexpr bool kInt4 = INT4;
   static constexpr int kNT = NT, kJ = J, kRows = NT * 4 * J;
   static constexpr int W = INT4 ? 4 : 8;
-  static constexpr int B = INT4 ? (NT == 2 ? 2 : 3) : 1;
+  static constexpr int B = INT4 ? 2 : 1;
   static constexpr int U = INT4 ? 2 : 1;
 };
 // Stages of the ring: as many as fit beside the other blocks of the SM, at most 4 (4 bits: 3).
