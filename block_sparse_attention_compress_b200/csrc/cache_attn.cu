@@ -44,7 +44,7 @@
 namespace nsa {
 namespace {
 
-constexpr int kTile = 16;         // tokens per step of a warp
+constexpr int kTile = 16;         // tokens of an MMA's M
 constexpr int kShort = 8, kLonger = 2;   // see the cutting of the work
 constexpr int kFlush = 32;        // tiles between two corrections of the accumulators
 constexpr float kLn2 = 0.6931471805599453f;
@@ -314,7 +314,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   float* sq_sc = reinterpret_cast<float*>(sq_last + NT * 256);
 
   // ---- which tiles are this block's: `left` of them from tile t of item (b, h, rt) on
-  asm volatile("griddepcontrol.launch_dependents;");   // the join may start to be set up
+  asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up; it waits before it reads
   // a step of all streams is 1.3 us (4 bits), a part's start and end about 5
   const int extra = 4 * streams;
   int b, h, rt, t = 0;
@@ -475,7 +475,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     const int each = (take + streams - 1) / streams;
     const int ta = first + min(take, ts * each), tb = first + min(take, (ts + 1) * each);
     // steps inside [all_lo, all_hi) are seen whole by every row of the block
-        const int all_lo = a.window > 0 ? max(0, sp.p0 + pl.last[rt] - a.window + 1) : 0, all_hi = sp.p0 + pl.first[rt] + 1;
+    const int all_lo = a.window > 0 ? max(0, sp.p0 + pl.last[rt] - a.window + 1) : 0, all_hi = sp.p0 + pl.first[rt] + 1;
 
     // the next tile to copy: its place in its page, and the page after that one, fetched ahead
     int cp_u = sp.base + ta * kStep, cp_j = 0, cp_off = 0, ahead = 0;
@@ -1063,7 +1063,9 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
   if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
-// Warps per block, blocks per SM, tiles of 16 tokens per step.
+// Warps per block, blocks per SM, tiles of 16 tokens per step.  4 bits: eight warps an SM with all the registers
+// they ask for; twelve of 168 spill (16 rows, 8 x 64K tokens: 175 us instead of 147), and one tile a step leaves a
+// warp too little that is independent (155).  bf16: the ring needs the shared memory.
 template <bool INT4, int NT, int J>
 struct Shape {
   static constexpr bool kInt4 = INT4;
@@ -1093,7 +1095,7 @@ constexpr int kSms = 148;
 constexpr int kWholeTokens = 128;
 
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
-  Plan p;
+  Plan p{};
   const int R = a.n_new * a.G;
   int W = 0, step = 0, resident = 0, rows = 0;
   with_shape(c.int4, R, [&](auto h) { W = h.W; step = kTile * h.U; resident = h.B; rows = h.kRows; });
