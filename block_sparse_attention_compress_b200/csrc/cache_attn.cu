@@ -957,21 +957,24 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       const int rr = x / (DV / 4), d = (x % (DV / 4)) * 4, col = rr % kCols, r = rt * pl.tile_rows + rr;
       const char* base = smem + (rr / kCols) * kWarpBytes;   // the first warp of the row's group
       const size_t step = (size_t)pl.row_groups * kWarpBytes;
-      float mm = kNone;
-#pragma unroll
-      for (int w = 0; w < W; ++w)
-        if (w < streams) mm = fmaxf(mm, reinterpret_cast<const float*>(base + w * step)[kCols * kRow + col]);
-      float ll = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mw[W], lw[W], mm = kNone, ll = 0.f;   // all streams' loads side by side
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        if (w >= streams) break;
-        const float* f = reinterpret_cast<const float*>(base + w * step);
-        const float lw = f[kCols * kRow + kCols + col], k = ex2(f[kCols * kRow + col] - mm);
-        if (lw == 0.f) continue;
-        const float4 y = *reinterpret_cast<const float4*>(f + col * kRow + d);
-        ll += k * lw;
-        acc.x += k * y.x; acc.y += k * y.y; acc.z += k * y.z; acc.w += k * y.w;
+        const float* f = reinterpret_cast<const float*>(base + w * step) + kCols * kRow + col;
+        mw[w] = w < streams ? f[0] : kNone;
+        lw[w] = w < streams ? f[kCols] : 0.f;
+      }
+      float4 y[W], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        mm = fmaxf(mm, mw[w]);
+        y[w] = lw[w] == 0.f ? acc : *reinterpret_cast<const float4*>(base + w * step + (col * kRow + d) * 4);
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float k = ex2(mw[w] - mm);
+        ll += k * lw[w];
+        acc.x += k * y[w].x; acc.y += k * y[w].y; acc.z += k * y[w].z; acc.w += k * y[w].w;
       }
       if (alone) {
         const size_t row = out_row(r);
