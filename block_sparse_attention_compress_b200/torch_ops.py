@@ -3,12 +3,13 @@ and the workspace with torch (device memory is all torch provides) and call
 the library's entry points on the current stream."""
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import (NSA_CACHE_BF16, NSA_CACHE_INT4, NSA_MODE_MOBA, NSA_MODE_NSA, NsaCache, NsaCacheAppendArgs,
-               NsaCacheAttentionArgs, make_config, nsa_cache_append, nsa_cache_attention,
-               nsa_cache_attention_workspace, nsa_cache_read, nsa_compress, nsa_decode, nsa_forward,
-               nsa_forward_varlen, nsa_workspace_size)
+               NsaCacheAttentionArgs, NsaError, load_library, make_config, nsa_cache_attention_workspace, nsa_compress,
+               nsa_decode, nsa_forward, nsa_forward_varlen, nsa_workspace_size)
 
 
 def n_cmp(T: int, l: int = 32, s: int = 16) -> int:
@@ -155,6 +156,7 @@ class KVCache:
                              d_v=d_v, page_size=page_size, n_pages=self.k.shape[0], max_pages=table.shape[1],
                              k=p(self.k), v=p(self.v), k_scale=p(self.k_scale), v_scale=p(self.v_scale),
                              page_table=p(table), status=p(self.status))
+        self._lib, self._ref = load_library(), ctypes.byref(self.desc)
         self._workspaces = {}   # bytes by (n, h_q, max_seqlen, window)
 
     @property
@@ -168,15 +170,21 @@ class KVCache:
     # A single token's calls take as long on the host as on the GPU: checks are plain conditions, and
     # their messages are made only when one fails.
 
-    def _call(self, fn, stream, *args):
-        """fn(cache, ..., stream) with the cache's device current; raises NsaError for a refusal."""
+    def _call(self, name, stream, *args):
+        """The library's entry `name` on this cache, with the cache's device current."""
         index = self.device.index
         if stream is None:
             stream = _current_stream(index)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        fn = getattr(self._lib, name)
         if torch.cuda.current_device() == index:
-            return fn(self.desc, *args, stream=stream)
-        with torch.cuda.device(index):
-            return fn(self.desc, *args, stream=stream)
+            st = fn(self._ref, *args, stream)
+        else:
+            with torch.cuda.device(index):
+                st = fn(self._ref, *args, stream)
+        if st:
+            raise NsaError(st, name)
 
     def _lengths(self, t, n, name):
         if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or not t.is_contiguous():
@@ -254,7 +262,7 @@ class KVCache:
                 self._like(q_out, q.shape, torch.bfloat16, "q_out")
             a.q, a.q_out, a.h_q = q.data_ptr(), q_out.data_ptr(), h_q
         if lead.numel():   # no tokens: nothing to do
-            self._call(nsa_cache_append, stream, a)
+            self._call("nsa_cache_append", stream, ctypes.byref(a))
         return q_out if q is not None else None
 
     def read(self, seqlens, n=None, *, cu_seqlens=None, total=None, k_out=None, v_out=None, stream=None):
@@ -279,8 +287,8 @@ class KVCache:
         else:
             self._like(v_out, shapes[1], torch.bfloat16, "v_out")
         if lead[-1]:
-            self._call(nsa_cache_read, stream, seqlens, cu_seqlens, 0 if packed else lead[1], lead[0] if packed else 0, k_out.data_ptr(),
-                       v_out.data_ptr())
+            self._call("nsa_cache_read", stream, seqlens.data_ptr(), cu_seqlens.data_ptr() if packed else None,
+                       0 if packed else lead[1], lead[0] if packed else 0, k_out.data_ptr(), v_out.data_ptr())
         return k_out, v_out
 
     def attend(self, q, seqlens, max_seqlen=None, *, softmax_scale=0.0, softcap=0.0, slopes=None, window=0, out=None,
@@ -313,9 +321,11 @@ class KVCache:
                 need = self._workspaces[key] = nsa_cache_attention_workspace(self.desc, a)
             if need:
                 workspace = self._new(q, (need,), stream, torch.uint8)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous on {self.device}")
         if workspace is not None:
             a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        self._call(nsa_cache_attention, stream, q.data_ptr(), a, out.data_ptr())
+        self._call("nsa_cache_attention", stream, q.data_ptr(), ctypes.byref(a), out.data_ptr())
         return out
 
     def attend_workspace(self, n, h_q, max_seqlen=None, window=0):

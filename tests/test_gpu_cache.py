@@ -570,6 +570,7 @@ def test_refusals_of_the_python_calls():
         lambda: c.attend(bfz(2, 1, 2, 64), ok, slopes=torch.zeros(3, device=DEV)),
         lambda: c.attend(bfz(2, 1, 2, 64), ok, lse=torch.zeros(2, 2, device=DEV)),
         lambda: c.attend(bfz(2, 1, 2, 64), ok, out=bfz(2, 1, 2, 32)),
+        lambda: c.attend(bfz(2, 1, 2, 64), ok, workspace=torch.zeros(1 << 20, dtype=torch.uint8)),
     ]
     for call in bad:
         with pytest.raises(ValueError):
