@@ -152,8 +152,8 @@ __device__ __forceinline__ void put_chunk(const CacheArgs& c, const Row& w, int 
 // A block's tokens, looked up by its first threads.
 // kFlight: heads (kReadFlight: units of 16 values) a thread has in flight.  Append with 2 at 4 blocks an SM
 // moves 64K tokens of (64, 4) heads in 622 us (3.44 GB, 5.5 TB/s), with 2 at 3 blocks in 735, with 4 at 2
-// blocks in 749, with 1 at 4 in 722; read with 2 gives back 128K tokens of 4 heads in 90 us, with 4 in 109.
-constexpr int kThreads = 256, kMaxTokens = 8, kFlight = 2, kReadFlight = 2;
+// blocks in 749, with 1 at 4 in 722; read with 2 gives back 128K tokens of 4 heads in 92 us, with 4 in 112.
+constexpr int kThreads = 256, kMaxTokens = 16, kFlight = 2, kReadFlight = 2;
 struct Place : Row {
   bool live;   // written (append) or there (read)
 };
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const CacheArgs c, 
   }
 }
 
-// Sixteen values (unit u of a row): the row itself (bf16), or their two words of codes and the group's (s, z).
+// Sixteen values of a row, chunks u and u + DIM / 16 (the threads of a warp then read and write 16 bytes next to
+// one another): the row itself (bf16), or two words of codes and their groups' (s, z).
 struct Sixteen {
   uint4 a, b;
 };
@@ -322,15 +323,17 @@ __device__ __forceinline__ Sixteen fetch(const CacheArgs& c, const Row& w, int h
   Sixteen r;
   if constexpr (!INT4) {
     const size_t row = ((size_t)w.page * c.page_size + w.place) * c.h_kv + h;
-    const uint4* src = reinterpret_cast<const uint4*>(pool) + row * (DIM / 8) + 2 * u;
+    const uint4* src = reinterpret_cast<const uint4*>(pool) + row * (DIM / 8) + u;
     r.a = __ldg(src);
-    r.b = __ldg(src + 1);
+    r.b = __ldg(src + DIM / 16);
   } else {
     const size_t row = ((size_t)w.page * c.h_kv + h) * c.page_size + w.place;
     const uint8_t* src = static_cast<const uint8_t*>(pool) + row * (DIM / 2);
-    r.a.x = load_codes<DIM, KEY>(src, 2 * u);
-    r.a.y = load_codes<DIM, KEY>(src, 2 * u + 1);
-    r.a.z = __ldg(reinterpret_cast<const uint32_t*>(KEY ? c.k_scale : c.v_scale) + row * (DIM / 32) + (u >> 1));
+    const uint32_t* sz = reinterpret_cast<const uint32_t*>(KEY ? c.k_scale : c.v_scale) + row * (DIM / 32);
+    r.a.x = load_codes<DIM, KEY>(src, u);
+    r.a.y = load_codes<DIM, KEY>(src, u + DIM / 16);
+    r.a.z = __ldg(sz + (u >> 2));
+    r.a.w = __ldg(sz + ((u + DIM / 16) >> 2));
   }
   return r;
 }
@@ -383,21 +386,23 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const CacheArgs c, const
     for (int f = 0; f < kReadFlight; ++f) {
       if (tok[f] >= n || s_place[tok[f]].seq < 0) continue;
       const size_t i = (size_t)i0 + tok[f];
-      uint4* dst = 2 * (y[f] < nk ? i * nk + y[f] : i * nv + y[f] - nk) + (y[f] < nk ? k_out : v_out);
+      const int z = y[f] - nk;
+      uint4* dst = z < 0 ? k_out + 2 * i * nk + y[f] / (DK / 16) * (DK / 8) + y[f] % (DK / 16)
+                         : v_out + 2 * i * nv + z / (DV / 16) * (DV / 8) + z % (DV / 16);
       if (!s_place[tok[f]].live) v[f].a = v[f].b = make_uint4(0, 0, 0, 0);
-      else if (INT4) v[f] = Sixteen{values_of(v[f].a.x, v[f].a.z), values_of(v[f].a.y, v[f].a.z)};
+      else if (INT4) v[f] = Sixteen{values_of(v[f].a.x, v[f].a.z), values_of(v[f].a.y, v[f].a.w)};
       dst[0] = v[f].a;
-      dst[1] = v[f].b;
+      dst[z < 0 ? DK / 16 : DV / 16] = v[f].b;
     }
   }
 }
 
-// Tokens a block takes: one while there are few of them, more once the blocks fill the GPU.
-int tokens_per_block(int rows) { return std::max(1, std::min(kMaxTokens, rows / (148 * 8))); }
+// Tokens a block takes: one while there are few of them, up to `most` once the blocks fill the GPU.
+int tokens_per_block(int rows, int most) { return std::max(1, std::min(most, rows / (148 * 8))); }
 
 template <int DK, int DV>
 cudaError_t append_dims(const CacheArgs& c, const RowsArgs& r, const AppendArgs& a, cudaStream_t st) {
-  const int n = tokens_per_block(r.rows), grid = (r.rows + n - 1) / n;
+  const int n = tokens_per_block(r.rows, 8), grid = (r.rows + n - 1) / n;
   if (c.int4) append_kernel<DK, DV, true><<<grid, kThreads, 0, st>>>(c, r, a, n);
   else append_kernel<DK, DV, false><<<grid, kThreads, 0, st>>>(c, r, a, n);
   return cudaGetLastError();
@@ -405,7 +410,8 @@ cudaError_t append_dims(const CacheArgs& c, const RowsArgs& r, const AppendArgs&
 
 template <int DK, int DV>
 cudaError_t read_dims(const CacheArgs& c, const RowsArgs& r, void* k_out, void* v_out, cudaStream_t st) {
-  const int n = tokens_per_block(r.rows), grid = (r.rows + n - 1) / n;
+  // about four units a thread: 12 tokens of 4 heads (128K of them 87 us; 6 tokens 96), 2 of 32 (16K: 62; 8 tokens 70)
+  const int n = tokens_per_block(r.rows, std::min(kMaxTokens, 1024 / (c.h_kv * (DK + DV) / 16))), grid = (r.rows + n - 1) / n;
   uint4 *k = static_cast<uint4*>(k_out), *v = static_cast<uint4*>(v_out);
   if (c.int4) read_kernel<DK, DV, true><<<grid, kThreads, 0, st>>>(c, r, k, v, n);
   else read_kernel<DK, DV, false><<<grid, kThreads, 0, st>>>(c, r, k, v, n);
