@@ -34,8 +34,8 @@
 //
 // Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 222 us, 6.0 TB/s.  32 x 64K tokens
 // in 4 bits, same heads: 490 us, 3.4 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 155 us, 4.3
-// TB/s.  In 4 bits the issue slots bound it, not HBM: about 540 instructions a tile of 16 tokens and 16 rows, of
-// which 108 unpack nibbles, at 2 a cycle and SM; logic at half rate, MMAs and fp32 products compete for
+// TB/s.  In 4 bits the issue slots bound it, not HBM: about 500 instructions a tile of 16 tokens and 16 rows, of
+// which 108 unpack nibbles, at 1.8 a cycle and SM; logic at half rate, MMAs and fp32 products compete for
 // the same slots (4 MMAs, 16 logic and 16 fma instructions take 58 cycles, not 32).
 #include <algorithm>
 
