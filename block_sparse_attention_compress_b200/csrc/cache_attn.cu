@@ -32,9 +32,9 @@
 // leaves a part in each block's slots and a second small kernel joins the parts by their maxima and
 // sums, in a fixed order.
 //
-// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 222 us, 6.0 TB/s.  32 x 64K tokens
-// in 4 bits, same heads: 490 us, 3.4 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 155 us, 4.3
-// TB/s.  In 4 bits the issue slots bound it, not HBM: about 500 instructions a tile of 16 tokens and 16 rows, of
+// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 215-222 us, 6.1 TB/s.  32 x 64K tokens
+// in 4 bits, same heads: 476-508 us, 3.4 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 146-157
+// us, 4.4 TB/s.  In 4 bits the issue slots bound it, not HBM: about 500 instructions a tile of 16 tokens and 16 rows, of
 // which 108 unpack nibbles, at 1.8 a cycle and SM; logic at half rate, MMAs and fp32 products compete for
 // the same slots (4 MMAs, 16 logic and 16 fma instructions take 58 cycles, not 32).
 #include <algorithm>
@@ -881,12 +881,18 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       } else {
 #pragma unroll
         for (int x = 0; x < U; ++x) {
-          uint32_t pb[NT][2];
+          // the weights as two bf16 terms: one alone made outputs 1.4 times as far off as their own rounding does.
+          // Free while HBM bounds the call; 64 rows a head, which the MMAs bound, take 254 us instead of 207 (16 x 16,800 tokens)
+          uint32_t pb[NT][2], rest[NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            pb[nt][0] = movmatrix(pack_bf16(s[x][nt][0], s[x][nt][1]));
-            pb[nt][1] = movmatrix(pack_bf16(s[x][nt][2], s[x][nt][3]));
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p0 = s[x][nt][2 * e], p1 = s[x][nt][2 * e + 1];
+              const uint32_t w = pack_bf16(p0, p1);
+              pb[nt][e] = movmatrix(w);
+              rest[nt][e] = movmatrix(pack_bf16(p0 - cache::bf16_lo(w), p1 - cache::bf16_hi(w)));
+            }
           const char* vrow = st + x * T::kBytes + T::kV + 2 * q4 * T::kRowV;
 #pragma unroll
           for (int i = 0; i < DV / 64; ++i) {
@@ -897,11 +903,15 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
             const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
             const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)   // word e holds dims 2 e and 2 e + 1 of the lane's eight
+            for (int e = 0; e < 4; ++e) {   // word e holds dims 2 e and 2 e + 1 of the lane's eight
+              const uint32_t a0 = __byte_perm(w0[e], w1[e], 0x5410), a1 = __byte_perm(w0[e], w1[e], 0x7632);
+              const uint32_t a2 = __byte_perm(w2[e], w3[e], 0x5410), a3 = __byte_perm(w2[e], w3[e], 0x7632);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_bf16(o[4 * i + e][nt], __byte_perm(w0[e], w1[e], 0x5410), __byte_perm(w0[e], w1[e], 0x7632),
-                         __byte_perm(w2[e], w3[e], 0x5410), __byte_perm(w2[e], w3[e], 0x7632), pb[nt][0], pb[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_bf16(o[4 * i + e][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                mma_bf16(o[4 * i + e][nt], a0, a1, a2, a3, rest[nt][0], rest[nt][1]);
+              }
+            }
           }
         }
       }

@@ -465,8 +465,8 @@ NSA_API nsa_status nsa_cache_read(const nsa_cache* cache, const int32_t* seqlens
  *   x = softcap * tanh(x / softcap)         if softcap > 0
  *   x = x + slopes[h] * (u - p)             if slopes (fp32 [h_q] device) is given
  * and softmax over u, in fp32; a query with p < 0 gives zeros.  4-bit keys enter exactly as
- * s (c - 8) + z.  The weights are rounded once before they meet the values: to bf16, or with 4-bit
- * values together with the group's s to f16 (s below 2^-20 of the largest s of that group of dims in
+ * s (c - 8) + z.  The weights are rounded once before they meet the values: to 16 bits (two bf16
+ * terms), or with 4-bit values together with the group's s to f16 (s below 2^-20 of the largest s of that group of dims in
  * the sequence loses digits, below 2^-30 its values count as z - 8 s).  lse (optional, fp32
  * [B, n_new, h_q]): the log of the sum of exp(x), -inf where
  * there is nothing to attend.  Values of tokens that no query of the sequence attends never
