@@ -111,7 +111,12 @@ class KVCache:
     tokens.
 
     A token that cannot be placed (page table entry, position or length out of range) is skipped,
-    and ``device_status()`` is then NSA_CODE_CACHE until ``status`` is zeroed."""
+    and ``device_status()`` is then NSA_CODE_CACHE until ``status`` is zeroed.
+
+    The calls run on the current stream, or on ``stream`` (a torch stream or its handle).  Outputs
+    and workspaces are then that stream's memory, and as ever with streams the caller makes it wait
+    for the inputs, and makes others wait for the outputs (and tells torch of their use there, with
+    ``record_stream``)."""
 
     def __init__(self, batch, max_len, h_kv, d_k, d_v, *, fmt="bf16", page_size=64, n_pages=None, device="cuda"):
         _need(fmt in ("bf16", "int4"), f"fmt is 'bf16' or 'int4', not {fmt!r}")
@@ -220,13 +225,15 @@ class KVCache:
         return t.data_ptr()
 
     def _new(self, like, shape, stream, dtype=torch.bfloat16):
+        """Memory for `stream`: from that stream's pool, since a block of another's may still be in use there."""
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=self.device)
+            with torch.cuda.stream(stream):
+                return like.new_empty(shape, dtype=dtype)
         if like.shape == shape and dtype is like.dtype:   # the quickest of torch's ways
-            t = torch.empty_like(like, memory_format=torch.contiguous_format)
-        else:
-            t = like.new_empty(shape, dtype=dtype)
-        if stream is not None:   # torch must not hand the memory out again before that stream is done
-            t.record_stream(torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
-        return t
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return like.new_empty(shape, dtype=dtype)
 
     def append(self, k, v, seqlens, *, cu_seqlens=None, cos_sin=None, interleaved=False, q=None, q_out=None, stream=None):
         """Write new tokens: k [batch, n, h_kv, d_k] and v [batch, n, h_kv, d_v] are the last n of

@@ -166,6 +166,41 @@ def test_kvcache_wants_a_gpu_and_sane_sizes():
         KVCache(1, 64, 1, 64, 64, device="cpu")
 
 
+def test_memory_for_a_given_stream_is_that_streams(monkeypatch):
+    """Outputs and workspaces of a call on a stream are allocated with that stream current, so that their memory
+    cannot be a block that work queued on another stream still uses."""
+    from block_sparse_attention_compress_b200.torch_ops import KVCache
+    current, seen = [], []
+
+    class Current:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    class Like:
+        shape, dtype, device = (2, 3), torch.bfloat16, torch.device("cpu")
+
+        def new_empty(self, shape, dtype):
+            seen.append(current[-1] if current else None)
+            return torch.empty(shape, dtype=dtype)
+
+    monkeypatch.setattr(torch.cuda, "stream", Current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: ("external", handle))
+    cache = KVCache.__new__(KVCache)
+    cache.device = torch.device("cpu")
+    mine = object()
+    for stream, want in ((mine, mine), (77, ("external", 77)), (0, ("external", 0)), (None, None)):
+        cache._new(Like(), (4, 5), stream)
+        assert seen.pop() == want
+    cache._new(Like(), (2, 3), mine)      # of the same shape as well
+    assert seen.pop() is mine
+
+
 # ------------------------------------------------------------------ the oracle's pins
 
 def test_rotation_turns_pairs_by_the_angle():
