@@ -76,7 +76,6 @@ nsa::CacheAttnArgs attention_args(const nsa_cache* c, const nsa_cache_attention_
   // a cap above 2^100 leaves every score that a softmax can tell apart as it is
   r.softcap = a->softcap < 0x1p100f ? a->softcap : 0.f;
   r.inv_softcap = r.softcap > 0.f ? std::fmin(1.f / r.softcap, 3e38f) : 0.f;
-  r.inv_softcap = a->softcap > 0.f ? 1.f / a->softcap : 0.f;
   r.n_new = a->n_new; r.h_q = a->h_q; r.G = a->h_q / c->h_kv; r.max_seqlen = a->max_seqlen;
   r.window = a->window < a->max_seqlen ? a->window : 0;   // reaches every token: none
   return r;

@@ -41,3 +41,23 @@ def test_memory_freed_behind_a_queue_of_another_stream_is_left_alone(handle):
         assert torch.equal(got, want)
         assert [int(s) for s in sums] == [need, want.numel()]
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("cap", [1e-30, 2e-39, 1e-44])
+def test_the_smallest_caps_leave_zero_scores_alone(fmt, cap):
+    """A query of zeros and a key of zeros score exactly 0, which any cap leaves at 0: equal weights, the mean of the values."""
+    lens = [70, 20]
+    g = gen(51)
+    c = KVCache(2, 70, 1, 64, 64, fmt=fmt, page_size=16, device=DEV)
+    k, v = bf((90, 1, 64), g), bf((90, 1, 64), g)
+    k[5] = k[80] = 0
+    c.append(k.to(DEV), v.to(DEV), i32(lens), cu_seqlens=i32([0, 70, 90]))
+    kept = (lambda x: co.through_4_bits(x)) if fmt == "int4" else (lambda x: x.double())
+    unit = co.quantise(v.unflatten(-1, (-1, 32)))[1].double().repeat_interleave(32, -1) * 8 if fmt == "int4" else v.double().abs()
+    held = [(kept(k)[a:b], kept(v)[a:b], unit[a:b]) for a, b in ((0, 70), (70, 90))]
+    q = bf((2, 2, 4, 64), g)
+    q[0, 0] = q[1, 1, 2] = 0
+    lse = torch.full((2, 2, 4), math.nan, device=DEV)
+    out = c.attend(q.to(DEV), i32(lens), 70, softcap=cap, lse=lse)
+    check_attention(out, lse, torch.zeros_like(q), held, lens)     # scores of 1e-30 and less: as if all were 0
