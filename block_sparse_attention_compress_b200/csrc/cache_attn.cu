@@ -869,7 +869,9 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
                 for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
                 const float y = z * top_s[gr] * 0x1p-24f;
-                if (fabsf(y) < 0x1p100f) {   // the eight lanes of a column agree
+                // below 2^60 a sum of all the run's stays finite through the factors 16, 2^24 and 2^20; a larger one belongs
+                // to offsets 2^50 times the spans and more, whose codes it need not cancel.  The eight lanes of a column agree
+                if (fabsf(y) < 0x1p60f) {
                   zacc[nt][gr][j] = 0.f;
                   o[2 * gr][nt][j] += y;
                   o[2 * gr][nt][j + 2] += 16.f * y;

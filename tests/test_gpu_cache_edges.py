@@ -61,3 +61,29 @@ def test_the_smallest_caps_leave_zero_scores_alone(fmt, cap):
     lse = torch.full((2, 2, 4), math.nan, device=DEV)
     out = c.attend(q.to(DEV), i32(lens), 70, softcap=cap, lse=lse)
     check_attention(out, lse, torch.zeros_like(q), held, lens)     # scores of 1e-30 and less: as if all were 0
+
+
+def looped(fmt, L, h_kv, d, page_rows, per_page=256):
+    """A cache of one sequence of L tokens whose pages are those of `page_rows` (lists of (k, v) [per_page, d] rows) over
+    and over: long runs of a warp without their memory."""
+    n = len(page_rows)
+    c = KVCache(1, L, h_kv, d, d, fmt=fmt, page_size=per_page, n_pages=n, device=DEV)
+    c.page_table.copy_((torch.arange(c.page_table.shape[1], device=DEV, dtype=torch.int32) % n)[None])
+    k, v = (torch.cat(x)[:, None].expand(-1, h_kv, -1).contiguous().to(DEV) for x in zip(*page_rows))
+    c.append(k, v, i32([n * per_page]), cu_seqlens=i32([0, n * per_page]))
+    return c
+
+
+@pytest.mark.parametrize("z", [29952.0, -1e20, 1e-20])
+def test_long_runs_of_constant_values_stay_what_they_are(z):
+    """Groups without a span (s = 0) over ten thousand and more tokens of a warp, equal weights: the value itself."""
+    L, d = 14_000_000, 64
+    v = torch.full((256, d), z).bfloat16()
+    v[:, 32:] = torch.tensor(3.0)
+    c = looped("int4", L, 1, d, [(torch.zeros(256, d).bfloat16(), v)])
+    lse = torch.zeros((1, 1, 1), device=DEV)
+    out = c.attend(torch.zeros((1, 1, 1, d), dtype=torch.bfloat16, device=DEV), i32([L]), L, lse=lse)
+    assert c.device_status() == 0
+    # weights of 1 and their sums in fp32: sums of up to 2^24 units are exact, the rest far below half a step of bf16
+    assert torch.equal(out.cpu()[0, 0, 0], v[0])
+    assert abs(float(lse) - math.log(L)) <= math.log(L) * 2 ** -20
