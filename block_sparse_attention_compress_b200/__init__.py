@@ -72,7 +72,8 @@ class NsaCacheAppendArgs(ctypes.Structure):
 
 
 class NsaCacheAttentionArgs(ctypes.Structure):
-    """Mirror of ``nsa_cache_attention_args`` in include/nsa.h."""
+    """Mirror of ``nsa_cache_attention_args`` in include/nsa.h.  (ctypes keeps the low 32 bits of an integer: the caller of
+    the mirrors checks ranges, as KVCache does.)"""
     _fields_ = [(n, ctypes.c_void_p) for n in ("seqlens", "slopes", "lse", "workspace")] + \
                [("workspace_bytes", ctypes.c_size_t), ("softmax_scale", ctypes.c_float),
                 ("softcap", ctypes.c_float)] + \
@@ -288,6 +289,8 @@ def nsa_cache_append(cache: NsaCache, args: NsaCacheAppendArgs, stream=None, che
 def nsa_cache_read(cache: NsaCache, seqlens, cu_seqlens, n_new: int, total_tokens: int, k_out, v_out, stream=None,
                    check: bool = True) -> int:
     """The last tokens of every sequence out of a paged cache as bf16 (see include/nsa.h)."""
+    if not all(-1 << 31 <= n < 1 << 31 for n in (n_new, total_tokens)):   # ctypes would keep the low 32 bits
+        raise ValueError("n_new and total_tokens: below 2^31")
     st = load_library().nsa_cache_read(ctypes.byref(cache), _ptr(seqlens), _ptr(cu_seqlens), int(n_new),
                                        int(total_tokens), _ptr(k_out), _ptr(v_out), _stream(stream, k_out))
     return _check(st, "nsa_cache_read") if check else st

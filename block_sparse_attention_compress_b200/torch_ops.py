@@ -100,6 +100,9 @@ def _need(ok, what):
         raise ValueError(what)
 
 
+_INT32 = 1 << 31   # the C entries' integers are below it, and ctypes would keep the low bits of a larger one
+
+
 class KVCache:
     """A paged key/value cache in bf16 or in 4 bits, with the three calls that work on it.
 
@@ -149,6 +152,7 @@ class KVCache:
         return self
 
     def _set(self, fmt, batch, h_kv, d_k, d_v, page_size, pools, table):
+        _need(max(batch, h_kv, d_k, d_v, page_size, pools[0].shape[0], table.shape[1]) < _INT32, "sizes must be below 2^31")
         self.fmt, self.batch, self.h_kv, self.d_k, self.d_v, self.page_size = fmt, batch, h_kv, d_k, d_v, page_size
         self.k, self.v, self.k_scale, self.v_scale = pools
         self.page_table = table
@@ -282,8 +286,8 @@ class KVCache:
         if (total if packed else n) is None:
             raise ValueError("read takes n, or cu_seqlens and total")
         lead = (int(total),) if packed else (self.batch, int(n))
-        if lead[-1] < 0:
-            raise ValueError("read takes a number of tokens")
+        if not 0 <= lead[-1] < _INT32:
+            raise ValueError("read takes a number of tokens, below 2^31")
         shapes = (*lead, self.h_kv, self.d_k), (*lead, self.h_kv, self.d_v)
         if k_out is None:
             k_out = self._new(seqlens, shapes[0], stream, torch.bfloat16)
@@ -315,6 +319,8 @@ class KVCache:
         else:
             self._like(out, (B, n, h_q, self.d_v), torch.bfloat16, "out")
         max_seqlen = self.max_len if max_seqlen is None else max_seqlen
+        if not (-_INT32 <= max_seqlen < _INT32 and -_INT32 <= window < _INT32):
+            raise ValueError("max_seqlen and window: below 2^31")
         a = NsaCacheAttentionArgs(self._lengths(seqlens, self.batch, "seqlens"),
                                   None if slopes is None else self._like(slopes, (h_q,), torch.float32, "slopes"),
                                   None if lse is None else self._like(lse, (B, n, h_q), torch.float32, "lse"),
@@ -337,6 +343,8 @@ class KVCache:
 
     def attend_workspace(self, n, h_q, max_seqlen=None, window=0):
         """Bytes of workspace attend() needs for n new tokens and h_q query heads."""
+        max_seqlen = self.max_len if max_seqlen is None else max_seqlen
+        if not all(-_INT32 <= x < _INT32 for x in (n, h_q, max_seqlen, window)):
+            raise ValueError("n, h_q, max_seqlen and window: below 2^31")
         return nsa_cache_attention_workspace(
-            self.desc, NsaCacheAttentionArgs(n_new=n, h_q=h_q, window=window,
-                                             max_seqlen=self.max_len if max_seqlen is None else max_seqlen))
+            self.desc, NsaCacheAttentionArgs(n_new=n, h_q=h_q, window=window, max_seqlen=max_seqlen))

@@ -201,6 +201,49 @@ def test_memory_for_a_given_stream_is_that_streams(monkeypatch):
     assert seen.pop() is mine
 
 
+def _on_cpu(batch=1, max_pages=4, page_size=16, h_kv=1, d=64):
+    """A KVCache over CPU memory: everything up to the library's entries works on it."""
+    from block_sparse_attention_compress_b200.torch_ops import KVCache
+    c = KVCache.__new__(KVCache)
+    c.fmt, c.batch, c.h_kv, c.d_k, c.d_v, c.page_size, c.device = "bf16", batch, h_kv, d, d, page_size, torch.device("cpu")
+    c.desc = nsa.NsaCache(format=nsa.NSA_CACHE_BF16, batch=batch, h_kv=h_kv, d_k=d, d_v=d, page_size=page_size,
+                          n_pages=batch * max_pages, max_pages=max_pages)
+    c._lib, c._ref, c._workspaces = nsa.load_library(), ctypes.byref(c.desc), {}
+    return c
+
+
+@pytest.mark.parametrize("kw", [dict(max_seqlen=2 ** 32 + 5), dict(max_seqlen=2 ** 31), dict(window=2 ** 32 + 100),
+                                dict(window=2 ** 31), dict(window=-2 ** 32 + 7)])
+def test_integers_beyond_32_bits_are_refused(lib, kw):
+    """ctypes would keep their low 32 bits: 2^32 + 5 would pass as 5."""
+    c = _on_cpu()
+    q, lens = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16), torch.ones(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="2\\^31"):
+        c.attend(q, lens, **kw)
+    with pytest.raises(ValueError, match="2\\^31"):
+        c.attend_workspace(1, 1, **kw)
+
+
+def test_row_counts_beyond_32_bits_are_refused(lib):
+    c = _on_cpu()
+    lens, cu = torch.ones(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for n in (2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(ValueError, match="2\\^31"):
+            c.read(lens, n)
+        with pytest.raises(ValueError, match="2\\^31"):
+            c.read(lens, cu_seqlens=cu, total=n)
+        with pytest.raises(ValueError, match="2\\^31"):
+            c.attend_workspace(n, 1)
+        with pytest.raises(ValueError, match="2\\^31"):
+            c.attend_workspace(1, n)
+        with pytest.raises(ValueError, match="2\\^31"):
+            nsa.nsa_cache_read(c.desc, 0, None, n, 0, 0, 0, stream=0)
+    from block_sparse_attention_compress_b200.torch_ops import KVCache
+    with pytest.raises(ValueError, match="2\\^31"):      # 2^32 + 1 pages a sequence, of which ctypes would keep one
+        KVCache.__new__(KVCache)._set("bf16", 1, 1, 64, 64, 16, (torch.zeros(1, 16, 1, 64),) * 2 + (None, None),
+                                      torch.zeros(1, dtype=torch.int32).expand(1, 2 ** 32 + 1))
+
+
 # ------------------------------------------------------------------ the oracle's pins
 
 def test_rotation_turns_pairs_by_the_angle():
