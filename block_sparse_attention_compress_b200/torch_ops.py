@@ -108,8 +108,8 @@ class KVCache:
 
     ``KVCache(batch, max_len, h_kv, d_k, d_v)`` allocates the pool (``fmt`` "bf16" or "int4"),
     a status word and a page table that gives every sequence its own pages in order; a program
-    with its own page allocator passes ``n_pages`` and writes ``page_table`` [batch, max_pages]
-    (int32) itself.  ``from_pools`` takes existing bf16 pools, such as
+    with its own page allocator passes ``n_pages`` and writes into ``page_table`` [batch, max_pages]
+    (int32) itself (the tensors of a cache stay: they are written into, not replaced).  ``from_pools`` takes existing bf16 pools, such as
     nsa_decode's caches.  Lengths (``seqlens``, int32 [batch] on the device) always count the new
     tokens.
 
@@ -154,12 +154,11 @@ class KVCache:
     def _set(self, fmt, batch, h_kv, d_k, d_v, page_size, pools, table):
         _need(max(batch, h_kv, d_k, d_v, page_size, pools[0].shape[0], table.shape[1]) < _INT32, "sizes must be below 2^31")
         self.fmt, self.batch, self.h_kv, self.d_k, self.d_v, self.page_size = fmt, batch, h_kv, d_k, d_v, page_size
-        self.k, self.v, self.k_scale, self.v_scale = pools
-        self.page_table = table
+        self._pools, self._page_table = pools, table
         self.device = self.k.device
         for t in (self.k, self.v, self.page_table):
             _need(t.is_cuda and t.device == self.device and t.is_contiguous(), "pools and page table: contiguous, on one GPU")
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         p = lambda t: t.data_ptr() if t is not None else None
         self.desc = NsaCache(format=NSA_CACHE_INT4 if fmt == "int4" else NSA_CACHE_BF16, batch=batch, h_kv=h_kv, d_k=d_k,
                              d_v=d_v, page_size=page_size, n_pages=self.k.shape[0], max_pages=table.shape[1],
@@ -167,6 +166,14 @@ class KVCache:
                              page_table=p(table), status=p(self.status))
         self._lib, self._ref = load_library(), ctypes.byref(self.desc)
         self._workspaces = {}   # bytes by (n, h_q, max_seqlen, window)
+
+    # The library has these tensors' addresses: their contents may be written, the attributes not be assigned.
+    k = property(lambda self: self._pools[0], doc="keys: bf16 [n_pages, page_size, h_kv, d_k], or codes")
+    v = property(lambda self: self._pools[1], doc="values, like the keys")
+    k_scale = property(lambda self: self._pools[2], doc="4 bits: (s, z) of the keys' groups")
+    v_scale = property(lambda self: self._pools[3], doc="4 bits: (s, z) of the values' groups")
+    page_table = property(lambda self: self._page_table, doc="int32 [batch, max_pages]")
+    status = property(lambda self: self._status, doc="int32 [1]: 0, or NSA_CODE_CACHE")
 
     @property
     def max_len(self):

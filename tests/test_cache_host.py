@@ -244,6 +244,14 @@ def test_row_counts_beyond_32_bits_are_refused(lib):
                                       torch.zeros(1, dtype=torch.int32).expand(1, 2 ** 32 + 1))
 
 
+@pytest.mark.parametrize("name", ["k", "v", "k_scale", "v_scale", "page_table", "status"])
+def test_tensors_of_a_cache_cannot_be_replaced(name):
+    """The library keeps their addresses: a new tensor in their place would free the old one under the kernels."""
+    from block_sparse_attention_compress_b200.torch_ops import KVCache
+    with pytest.raises(AttributeError):
+        setattr(KVCache.__new__(KVCache), name, torch.zeros(1))
+
+
 # ------------------------------------------------------------------ the oracle's pins
 
 def test_rotation_turns_pairs_by_the_angle():
