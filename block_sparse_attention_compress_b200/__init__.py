@@ -164,6 +164,16 @@ def _stream(stream, *tensors) -> int | None:
     return None
 
 
+def _cache_stream(stream, *tensors) -> int | None:
+    """As _stream; where no tensor tells the device (the cache's structs hold addresses), torch's current stream."""
+    handle = _stream(stream, *tensors)
+    if handle is None:
+        import torch
+        if torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream
+    return handle
+
+
 def make_config(**fields) -> NsaConfig:
     """Build an NsaConfig; tensors given for pointer fields are replaced by their addresses."""
     cfg = NsaConfig()
@@ -281,8 +291,9 @@ def nsa_decode(q, k_cache, v_cache, kc_cache, vc_cache, seqlens, max_seqlen: int
 
 
 def nsa_cache_append(cache: NsaCache, args: NsaCacheAppendArgs, stream=None, check: bool = True) -> int:
-    """Write new tokens into a paged cache, keys rotated on the way (see include/nsa.h)."""
-    st = load_library().nsa_cache_append(ctypes.byref(cache), ctypes.byref(args), _stream(stream))
+    """Write new tokens into a paged cache, keys rotated on the way, on torch's current stream unless one is given
+    (see include/nsa.h)."""
+    st = load_library().nsa_cache_append(ctypes.byref(cache), ctypes.byref(args), _cache_stream(stream))
     return _check(st, "nsa_cache_append") if check else st
 
 
@@ -292,14 +303,14 @@ def nsa_cache_read(cache: NsaCache, seqlens, cu_seqlens, n_new: int, total_token
     if not all(-1 << 31 <= n < 1 << 31 for n in (n_new, total_tokens)):   # ctypes would keep the low 32 bits
         raise ValueError("n_new and total_tokens: below 2^31")
     st = load_library().nsa_cache_read(ctypes.byref(cache), _ptr(seqlens), _ptr(cu_seqlens), int(n_new),
-                                       int(total_tokens), _ptr(k_out), _ptr(v_out), _stream(stream, k_out))
+                                       int(total_tokens), _ptr(k_out), _ptr(v_out), _cache_stream(stream, k_out))
     return _check(st, "nsa_cache_read") if check else st
 
 
 def nsa_cache_attention(cache: NsaCache, q, args: NsaCacheAttentionArgs, out, stream=None, check: bool = True) -> int:
     """Attention of the newest tokens over a paged cache (see include/nsa.h)."""
     st = load_library().nsa_cache_attention(ctypes.byref(cache), _ptr(q), ctypes.byref(args), _ptr(out),
-                                            _stream(stream, q))
+                                            _cache_stream(stream, q))
     return _check(st, "nsa_cache_attention") if check else st
 
 

@@ -252,6 +252,27 @@ def test_tensors_of_a_cache_cannot_be_replaced(name):
         setattr(KVCache.__new__(KVCache), name, torch.zeros(1))
 
 
+def test_calls_by_addresses_run_on_the_current_stream(monkeypatch):
+    """The structs tell no device and no stream: torch's current stream it is, not the default one."""
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: streams.append(args[-1]) or nsa.NSA_OK
+
+    class Current:
+        cuda_stream = 4711
+
+    streams = []
+    monkeypatch.setattr(nsa, "load_library", lambda: Library())
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Current)
+    c = _cache()
+    for stream, want in ((None, 4711), (0, 0), (12, 12)):
+        nsa.nsa_cache_append(c, _append(), stream=stream)
+        nsa.nsa_cache_read(c, 0x300000, None, 1, 0, 0x700000, 0x800000, stream=stream)
+        nsa.nsa_cache_attention(c, 0x700000, _attn(), 0x800000, stream=stream)
+        assert streams[-3:] == [want] * 3
+
+
 # ------------------------------------------------------------------ the oracle's pins
 
 def test_rotation_turns_pairs_by_the_angle():
