@@ -96,6 +96,15 @@ __device__ __forceinline__ void fma_columns(float& x, float& y, float a, float b
     y = r.y;
   }
 }
+// o += y, rounded
+__device__ __forceinline__ void add_to(float (&o)[4], const float (&y)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const float2 r = f2_unpack(f2_add(f2_pack(o[e], o[e + 1]), f2_pack(y[e], y[e + 1])));
+    o[e] = r.x;
+    o[e + 1] = r.y;
+  }
+}
 template <int J>
 __device__ __forceinline__ float2 mul_columns(float a, float b, float f) {
   if constexpr (J == 1) return make_float2(a * f, 0.f);
@@ -883,8 +892,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       } else {
 #pragma unroll
         for (int x = 0; x < U; ++x) {
-          // the weights as two bf16 terms: one alone made outputs 1.4 times as far off as their own rounding does.
-          // Free while HBM bounds the call; 64 rows a head, which the MMAs bound, take 254 us instead of 207 (16 x 16,800 tokens)
+          // the weights as two bf16 terms (2^-18): one alone made outputs 1.4 times as far off as their own rounding does.
+          // And every tile's sum is added to the accumulators by itself, rounded: as the MMA's C they lost 2^-18 of the mean
+          // value over 3,200 tiles.  1 or 2% while HBM bounds the call; rows beyond 16 a head, which the MMAs bound, pay (16 x
+          // 16,800 tokens of 4 heads): the second term 110 -> 134 us for 32 rows, 207 -> 254 for 64; the sums another 5%
           uint32_t pb[NT][2], rest[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -910,8 +921,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
               const uint32_t a2 = __byte_perm(w2[e], w3[e], 0x5410), a3 = __byte_perm(w2[e], w3[e], 0x7632);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                mma_bf16(o[4 * i + e][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-                mma_bf16(o[4 * i + e][nt], a0, a1, a2, a3, rest[nt][0], rest[nt][1]);
+                float y[4];   // the tile's own sum: the MMA cuts off what the accumulator's last place does not hold
+                mma_bf16_first(y, a0, a1, a2, a3, rest[nt][0], rest[nt][1]);
+                mma_bf16(y, a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                add_to(o[4 * i + e][nt], y);
               }
             }
           }

@@ -87,3 +87,92 @@ def test_long_runs_of_constant_values_stay_what_they_are(z):
     # weights of 1 and their sums in fp32: sums of up to 2^24 units are exact, the rest far below half a step of bf16
     assert torch.equal(out.cpu()[0, 0, 0], v[0])
     assert abs(float(lse) - math.log(L)) <= math.log(L) * 2 ** -20
+
+
+def key_reach(fmt, q, k):
+    """The largest scale sum |q||k| of q [h, d] over k [L, d]; 4 bits: |k| as the kernel adds it up, 15 s + |z - 8 s|."""
+    k = k.double().abs()
+    if fmt == "int4":
+        _, s, z = co.quantise(k.bfloat16().unflatten(-1, (-1, 32)))
+        k = (15 * s + (z - 8 * s).abs()).double().repeat_interleave(32, -1)
+    return float((q.double().abs() @ k.T).max()) / math.sqrt(k.shape[-1])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("G,n", [(1, 1), (4, 1), (8, 1), (16, 1), (16, 4)])
+@pytest.mark.parametrize("fmt", ["bf16"])
+def test_weights_are_exact_far_below_the_outputs_rounding(fmt, dk, dv, G, n):
+    """Values that almost cancel under the weights of the (equal) queries, so that the output's own rounding (2^-8 of little)
+    hides nothing.  Allowed: weights of two terms, bf16 2^-18 each (2^-16 granted), f16 2^-22; a score's error e twice, with
+    e = 16 roundings of 2^-23 or less of scale sum |q||k| and 2^-20 for the exponential; sums of few terms, 2^-20."""
+    g = gen(60 + G + dk)
+    L, h_kv = 5 + n, 2
+    k, q = bf((L, h_kv, dk), g), bf((1, 1, 1, dk), g, 0.1).expand(1, n, h_kv * G, dk).contiguous()
+    k[:, 1] = k[:, 0]
+    v = bf((L, h_kv, dv), g)
+    kept = (lambda x: co.through_4_bits(x)) if fmt == "int4" else (lambda x: x.double())
+    kk = kept(k)
+    x = kk[:, 0] @ q[0, 0, 0].double() / math.sqrt(dk)
+    p = torch.exp(x - x.max())
+    # the first token is seen by every query; what the others up to the first query's position weigh, it takes back
+    seen = slice(1, L - n + 1)
+    v[0] = (-(p[seen, None, None] * kept(v)[seen]).sum(0) / p[0]).bfloat16()
+    v[L - n + 1:] = 0
+    c = KVCache(1, L, h_kv, dk, dv, fmt=fmt, page_size=16, device=DEV)
+    c.append(k.to(DEV), v.to(DEV), i32([L]), cu_seqlens=i32([0, L]))
+    out = c.attend(q.to(DEV), i32([L]), L).cpu().double()[0]
+    ref, _, mag = co.attend(q[0], kk, kept(v))
+    e = key_reach(fmt, q[0, 0, :1], k[:, 0]) * 2 ** -19 + 2 ** -20
+    unit = mag
+    if fmt == "int4":
+        s = co.quantise(v.unflatten(-1, (-1, 32)))[1].double().repeat_interleave(32, -1) * 8
+        unit = co.attend(q[0], kk, s)[2] + mag
+    bound = ref.abs() * 2 ** -8 + (2 ** -16 if fmt == "bf16" else 2 ** -20) * unit + (2 * e + 2 ** -20) * mag
+    worst = float(((out - ref).abs() / bound).max())
+    assert worst <= 1.01, worst
+
+
+@pytest.mark.parametrize("fmt", ["bf16"])
+@pytest.mark.parametrize("G,pages", [(1, 1024), (8, 1024), (16, 1024), (16, 1)])
+def test_long_sums_do_not_drift(fmt, G, pages):
+    """Equal weights over 60 million tokens (3,200 tiles a warp) whose values cancel exactly: `up` pages of positive values
+    from 2^-12 to 1, then a page of the negatives of one of them times `up`, and so on until each of the `pages` different
+    ones has come up as often as down.  A warp's sum of a dim climbs to A, about 256 up mean values, and falls again.
+
+    Cut off, a sum or its addends lose up to a unit of the sum's last place (2^-23 A) at every tile, always towards zero.
+    Rounded, a tile's error is at most half a unit either way: 2^-24 A / 16 a token whatever the tiles, 2^-15 (up = 32) or 2^-20
+    (up = 1) mean values.  With the sum a multiple of its unit, that error is the tile's own wherever it comes, so those of T = 16
+    pages different tiles average out: eight standard deviations, 8 2^-23 A / (16 sqrt(12 T)), with A 1.3 times as large as
+    above for what is left over from one climb to the next: 2^-19.4 or 2^-24.4 for 1024 pages.  A step of one or two tiles
+    (32 tokens) cut off at each of up to three products is less than 3 2^-23 32 / 32 = 2^-21.4."""
+    g = gen(70)
+    d, page, up = 64, 256, 32 if fmt == "bf16" else 1
+    cycle = torch.arange(pages)
+    climbs = (cycle[:, None] * up + torch.arange(up)) % pages
+    order = torch.cat((climbs, cycle[:, None] + pages), 1).flatten().int()
+    order = order.repeat(60_000_000 // (page * order.numel()))
+    L = page * order.numel()
+    c = KVCache(1, L, 1, d, d, fmt=fmt, page_size=page, n_pages=2 * pages, device=DEV)
+    c.page_table.copy_(order[None])
+    spread = lambda *shape: torch.exp2(-12 * torch.rand(shape, generator=g))
+    if fmt == "bf16":
+        v = spread(pages, page, 1, d).bfloat16()
+        c.v.copy_(torch.cat((v, -up * v)))
+        mean = v.double().mean((0, 1, 2))
+    else:     # codes 1 .. 15 and 16 less them; s (c - 8) + z with z above 8 s, and z negated
+        nib = torch.randint(1, 16, (pages, 1, page, d), generator=g, dtype=torch.uint8)
+        s = spread(pages, 1, page, d // 32).bfloat16()
+        z = (8.5 * s.float()).bfloat16()
+        byte = lambda x: x[..., 0::2] | (x[..., 1::2] << 4)
+        c.v.copy_(torch.cat((byte(nib), byte(16 - nib))))
+        c.v_scale.copy_(torch.cat((torch.stack((s, z), -1), torch.stack((s, -z), -1))))
+        _, back = c.read(i32([page]), page)
+        assert (back > 0).all()
+        mean = 8.5 * s.double().mean()
+    out = c.attend(torch.zeros((1, 1, G, d), dtype=torch.bfloat16, device=DEV), i32([L]), L)
+    assert c.device_status() == 0
+    worst = float((out.cpu().double().abs() / mean).max())
+    rounded = 2 ** -19.4 if up > 1 else 2 ** -24.4
+    if pages == 1:
+        rounded = 2 ** -15 if up > 1 else 2 ** -20
+    assert worst <= rounded + 2 ** -21.4, math.log2(worst)
