@@ -19,12 +19,16 @@
 // the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as more MMAs with
 // the stored pairs as A and the groups' query sums (three bf16 terms: 24 bits) as B.
 //
-// Values in 4 bits: the same pairs of subnormals, by two tokens of a dim.  A token's weight is
-// P s 2^k in f16 (one rounding, 2^-11), k by group from the largest s met so far, so that weights
-// stay below 2^15: full digits down to scales 2^-20 of the largest, nothing below 2^-30 of it.  P (z - 8 s)
-// is summed in fp32.  The tensor cores cut off sums instead of rounding them (measured: 4096 steps
-// lose 2e-4), so every 32 tiles the offset's sum is taken into the accumulators, which leaves them at
-// the size of the result.
+// Values in 4 bits: nibbles become s 2^k (c - 8) in f16, pairs of two tokens of a dim, exactly (at most 11 bits):
+// three instructions a pair (mask on the exponent of 1024, subtract, multiply), the same for every row.  k by group
+// from the largest s met so far: full digits down to scales 2^-28 of the largest, nothing below 2^-36 of it.  Weights
+// are two f16 terms (2^-22, and down to 2^-32 of the largest), P z is summed in fp32.  P s 2^k as one f16, against codes as
+// subnormals, was 10% (one row a head) to 15% (16 rows) faster, but made outputs differ from 32-bit arithmetic by 1.3e-3 of
+// their size instead of 1e-4.
+//
+// The tensor cores cut off sums instead of rounding them, always towards zero (as the MMA's C, an accumulator lost 2^-18 of
+// the mean value over 3,200 tiles), so a step's products are summed by themselves and join the accumulators rounded: 5%
+// of the time at 16 rows in 4 bits, nothing with fewer.
 //
 // Every warp copies its own tiles of 16 tokens into a ring in shared memory (cp.async, no block-wide
 // waits).  The tiles of all sequences and heads are laid end to end and cut into equal runs, one
@@ -32,11 +36,10 @@
 // leaves a part in each block's slots and a second small kernel joins the parts by their maxima and
 // sums, in a fixed order.
 //
-// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 215-222 us, 6.1 TB/s.  32 x 64K tokens
-// in 4 bits, same heads: 476-508 us, 3.4 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 146-157
-// us, 4.4 TB/s.  In 4 bits the issue slots bound it, not HBM: about 500 instructions a tile of 16 tokens and 16 rows, of
-// which 108 unpack nibbles, at 1.8 a cycle and SM; logic at half rate, MMAs and fp32 products compete for
-// the same slots (4 MMAs, 16 logic and 16 fma instructions take 58 cycles, not 32).
+// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 215-231 us, 5.8-6.2 TB/s.  32 x 64K tokens
+// in 4 bits, same heads: 579 us, 2.9 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 171 us, 3.9
+// TB/s.  In 4 bits the issue slots bound it, not HBM: logic at half rate, MMAs and fp32 products compete for the same
+// slots (4 MMAs, 16 logic and 16 fma instructions take 58 cycles, not 32).
 #include <algorithm>
 
 #include "cache.cuh"
@@ -46,7 +49,6 @@ namespace {
 
 constexpr int kTile = 16;         // tokens of an MMA's M
 constexpr int kShort = 8, kLonger = 2;   // see the cutting of the work
-constexpr int kFlush = 32;        // tiles between two corrections of the accumulators
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -105,12 +107,20 @@ __device__ __forceinline__ void add_to(float (&o)[4], const float (&y)[4]) {
     o[e + 1] = r.y;
   }
 }
-template <int J>
-__device__ __forceinline__ float2 mul_columns(float a, float b, float f) {
-  if constexpr (J == 1) return make_float2(a * f, 0.f);
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f2_pack(a, b)), "l"(f2_pack(f, f)));
-  return f2_unpack(d);
+// x cut to the 11 bits that f16 holds of it
+__device__ __forceinline__ float leading11(float x) { return __uint_as_float(__float_as_uint(x) & 0xffffe000u); }
+// s (c - 8) of the codes c in bits 0..3 (4..7) of each half of w, s f16: 1024 + c (1024 + 16 c) is the code below f16's
+// exponent of 2^10; the rest is exact (4 bits times 8 are at most 11: 8 s is s shifted)
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t low_values(uint32_t w, uint32_t s) {
+  const __half2 c = __hsub2(as_half2((w & 0x000f000fu) | 0x64006400u), as_half2(0x64086408u));
+  const __half2 v = __hmul2(c, as_half2(s));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t high_values(uint32_t w, uint32_t s) {
+  const __half2 c = __hfma2(as_half2((w & 0x00f000f0u) | 0x64006400u), as_half2(0x2c002c00u), as_half2(0xd480d480u));   // / 16 - 72
+  const __half2 v = __hmul2(c, as_half2(s));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }   // of a normal one
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // -126 <= e <= 127
@@ -290,9 +300,13 @@ struct Walk {
 // Shared memory of a block: a ring (and later the joined rows) per warp, then in 4 bits the queries of
 // each row group: per tile of 8 rows the B fragments [DK / 32][32 lanes] x 16 bytes, the group sums'
 // [32 lanes] x (16 + 8) bytes and the rows' factors.
+template <bool INT4, int DV, int U>
+constexpr int scale_smem() {
+  return INT4 ? U * kTile * (DV / 32) * 2 : 0;
+}
 template <bool INT4, int DK, int DV, int NT, int U, int S>
 constexpr int warp_smem() {
-  return std::max(S * U * Stage<INT4, DK, DV>::kBytes, NT * 8 * (DV + 4 + 2) * 4);
+  return std::max(S * U * Stage<INT4, DK, DV>::kBytes + scale_smem<INT4, DV, U>(), NT * 8 * (DV + 4 + 2) * 4);
 }
 template <bool INT4, int DK, int NT>
 constexpr int query_smem() {
@@ -305,6 +319,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
                   float* __restrict__ part_o) {
   using T = Stage<INT4, DK, DV>;
   constexpr int NG = DK / 32, NH = DV / 32, MT = DV / 16, KS = DK / 16;
+  // 4 bits: the reference lies 2^7 below the maximum, so that f16 holds weights down to 2^-32 of it (and the largest, 2^15)
+  constexpr float kAbove = INT4 ? 7.f : 0.f;
   // a warp's rows: J of a lane's two columns hold one
   constexpr int kCols = NT * 4 * J, kRow = DV + 4;
   const auto row_of = [](int nt, int column) { return J == 2 ? nt * 8 + column : column >> 1; };
@@ -649,7 +665,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       }
     }
 
-    int stage = 0, since = 0;
+    int stage = 0;
     for (int tile = ta; tile < tb; ++tile) {
       cp_async_wait<S - 2>();
       __syncwarp();
@@ -775,7 +791,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           top[nt][j] = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
 #pragma unroll
           for (int x = 1; x < U; ++x) top[nt][j] = fmaxf(top[nt][j], fmaxf(s[x][nt][j], s[x][nt][j + 2]));
-          move |= top[nt][j] > m[nt][j] + 8.f;
+          move |= top[nt][j] > m[nt][j] + (8.f + kAbove);
         }
       if (__any_sync(0xffffffffu, move)) {
         float grow[INT4 ? NH : 1];
@@ -786,8 +802,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
             x = __reduce_max_sync(0xffffffffu, x < 0x7f80u ? x : 0u);   // a NaN shows in its products
             x = max(x, max_s[gr]);
             x = x ? x | 0x7fu : 0u;             // all of the binade
-            // s 2^k < 2^7: k = 6 - (exponent of s)
-            const float to = pow2(x ? min(6 - ((int)(x >> 7) - 127), 100) : 100);
+            // s 2^k < 2^12, so that 8 s 2^k is an f16: k = 11 - (exponent of s)
+            const float to = pow2(x ? min(11 - ((int)(x >> 7) - 127), 100) : 100);
             grow[gr] = to * inverse_pow2(top_s[gr]);
             top_s[gr] = to;
             max_s[gr] = x;
@@ -800,7 +816,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
             float x = top[nt][j];
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            x = fmaxf(x, m[nt][j]);
+            x = fmaxf(x - kAbove, m[nt][j]);
             const float k = ex2(m[nt][j] - x);
             m[nt][j] = x;
             l[nt][j] *= k;
@@ -811,8 +827,8 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               const float f = INT4 ? k * grow[INT4 ? mt / 2 : 0] : k;
-              o[mt][nt][j] *= f;
-              o[mt][nt][j + 2] *= f;
+#pragma unroll
+              for (int e = j; e < 4; e += J) o[mt][nt][e] *= f;   // one row to two columns: both
             }
           }
       }
@@ -829,65 +845,78 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 
       // ---- O^T += V^T P^T
       if constexpr (INT4) {
+        // the step's scales times their 2^k as f16 pairs of neighbouring tokens
+        __half* scales = reinterpret_cast<__half*>(ring + S * U * T::kBytes);
+        const int tok = lane % kStep;
+#pragma unroll
+        for (int gr = 0; gr < NH; ++gr)
+          scales[((tok >> 1) * NH + gr) * 2 + (tok & 1)] = __float2half_rn(cache::bf16_lo(sv[gr]) * top_s[gr]);
+        __syncwarp();
+        // the offsets' sum; the weights as two f16 terms: MMAs of their own, or (one row to two columns) the row's other column
+        uint32_t ph[U][NT][2], pl[J == 2 ? U : 1][NT][2];
 #pragma unroll
         for (int x = 0; x < U; ++x) {
-          const char* sx = st + x * T::kBytes;
-          uint32_t vs[2][NH], vw[4][NH / 2];   // rows g8, g8 + 8; tokens 2q, 2q+1, 2q+8, 2q+9
+          uint32_t vs[2][NH];   // rows g8, g8 + 8
 #pragma unroll
-          for (int j = 0; j < 2; ++j) lds_words<NH>(vs[j], sx + T::kVs + (g8 + 8 * j) * T::kRowVs);
+          for (int j = 0; j < 2; ++j) lds_words<NH>(vs[j], st + x * T::kBytes + T::kVs + (g8 + 8 * j) * T::kRowVs);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = 2 * q4 + (j & 1) + 8 * (j >> 1), at = g8 * (NH * 2);
-            lds_words<NH / 2>(vw[j], sx + T::kV + row * T::kRowV + T::value_unit(row, at / 16) * 16 + at % 16);
-          }
+          for (int nt = 0; nt < NT; ++nt) {
+            const float(&p)[4] = s[x][nt];
 #pragma unroll
-          for (int gr = 0; gr < NH; ++gr) {
-            uint32_t pb[NT][2];
-            const float r0s = cache::bf16_lo(vs[0][gr]), r1s = cache::bf16_lo(vs[1][gr]);
-            const float s0 = r0s * top_s[gr], s1 = r1s * top_s[gr];
-            const float z0 = fmaf(-8.f, r0s, cache::bf16_hi(vs[0][gr])), z1 = fmaf(-8.f, r1s, cache::bf16_hi(vs[1][gr]));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float(&p)[4] = s[x][nt];
-              const float2 w0 = mul_columns<J>(p[0], p[1], s0), w1 = mul_columns<J>(p[2], p[3], s1);
-              pb[nt][0] = movmatrix(pack_f16(w0.x, w0.y));
-              pb[nt][1] = movmatrix(pack_f16(w1.x, w1.y));
-              fma_columns<J>(zacc[nt][gr][0], zacc[nt][gr][J - 1], p[0], p[1], z0);
-              fma_columns<J>(zacc[nt][gr][0], zacc[nt][gr][J - 1], p[2], p[3], z1);
+            for (int gr = 0; gr < NH; ++gr) {
+              fma_columns<J>(zacc[nt][gr][0], zacc[nt][gr][J - 1], p[0], p[1], cache::bf16_hi(vs[0][gr]));
+              fma_columns<J>(zacc[nt][gr][0], zacc[nt][gr][J - 1], p[2], p[3], cache::bf16_hi(vs[1][gr]));
             }
-            const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
-            const uint32_t lo = __byte_perm(vw[0][gr / 2], vw[1][gr / 2], sel), lo8 = lo >> 8;
-            const uint32_t hi = __byte_perm(vw[2][gr / 2], vw[3][gr / 2], sel), hi8 = hi >> 8;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(o[2 * gr][nt], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, pb[nt][0], pb[nt][1]);
-              mma_f16(o[2 * gr + 1][nt], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, pb[nt][0],
-                      pb[nt][1]);
+            for (int e = 0; e < 2; ++e) {
+              const float h0 = leading11(p[2 * e]);
+              if constexpr (J == 2) {
+                const float h1 = leading11(p[2 * e + 1]);
+                const float2 rest = f2_unpack(f2_fma(f2_pack(h0, h1), f2_pack(-1.f, -1.f), f2_pack(p[2 * e], p[2 * e + 1])));
+                ph[x][nt][e] = movmatrix(pack_f16(h0, h1));
+                pl[x][nt][e] = movmatrix(pack_f16(rest.x, rest.y));
+              } else {
+                ph[x][nt][e] = movmatrix(pack_f16(h0, p[2 * e] - h0));
+              }
             }
           }
         }
-        if (++since == kFlush / U) {   // take the offset's sum into the accumulators
-          since = 0;
+        uint32_t vw[U][4][NH / 2];   // tokens 2q, 2q+1, 2q+8, 2q+9
 #pragma unroll
-          for (int gr = 0; gr < NH; ++gr)
+        for (int x = 0; x < U; ++x)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < 4; ++j) {
+            const int row = 2 * q4 + (j & 1) + 8 * (j >> 1), at = g8 * (NH * 2);
+            lds_words<NH / 2>(vw[x][j], st + x * T::kBytes + T::kV + row * T::kRowV + T::value_unit(row, at / 16) * 16 + at % 16);
+          }
 #pragma unroll
-              for (int j = 0; j < J; ++j) {
-                float z = zacc[nt][gr][j];
+        for (int gr = 0; gr < NH; ++gr) {
+          float y[2][NT][4];   // the step's own sum
 #pragma unroll
-                for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-                const float y = z * top_s[gr] * 0x1p-24f;
-                // below 2^60 a sum of all the run's stays finite through the factors 16, 2^24 and 2^20; a larger one belongs
-                // to offsets 2^50 times the spans and more, whose codes it need not cancel.  The eight lanes of a column agree
-                if (fabsf(y) < 0x1p60f) {
-                  zacc[nt][gr][j] = 0.f;
-                  o[2 * gr][nt][j] += y;
-                  o[2 * gr][nt][j + 2] += 16.f * y;
-                  o[2 * gr + 1][nt][j] += y;
-                  o[2 * gr + 1][nt][j + 2] += 16.f * y;
+          for (int x = 0; x < U; ++x) {
+            const uint32_t* pair = reinterpret_cast<const uint32_t*>(scales) + (8 * x + q4) * NH + gr;
+            const uint32_t s01 = pair[0], s89 = pair[4 * NH], sel = (gr & 1) ? 0x7632u : 0x5410u;
+            const uint32_t lo = __byte_perm(vw[x][0][gr / 2], vw[x][1][gr / 2], sel);
+            const uint32_t hi = __byte_perm(vw[x][2][gr / 2], vw[x][3][gr / 2], sel);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t wl = lo >> (8 * e), wh = hi >> (8 * e);
+              const uint32_t a0 = low_values(wl, s01), a1 = high_values(wl, s01), a2 = low_values(wh, s89), a3 = high_values(wh, s89);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if constexpr (J == 2) {
+                  if (x == 0) mma_f16_first(y[e][nt], a0, a1, a2, a3, pl[x][nt][0], pl[x][nt][1]);
+                  else mma_f16(y[e][nt], a0, a1, a2, a3, pl[x][nt][0], pl[x][nt][1]);
                 }
+                if (J == 1 && x == 0) mma_f16_first(y[e][nt], a0, a1, a2, a3, ph[x][nt][0], ph[x][nt][1]);
+                else mma_f16(y[e][nt], a0, a1, a2, a3, ph[x][nt][0], ph[x][nt][1]);
               }
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) add_to(o[2 * gr + e][nt], y[e][nt]);
         }
       } else {
 #pragma unroll
@@ -964,9 +993,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 #pragma unroll
             for (int d = 4; d <= 16; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
             const float down = inverse_pow2(top_s[gr]);
+            const auto sum = [&](const float(&y)[4], int e) { return J == 2 ? y[e + j] : y[e] + y[e + 1]; };
             *reinterpret_cast<float4*>(row + 32 * gr + 4 * g8) =
-                make_float4(fmaf(o[2 * gr][nt][j] * 0x1p24f, down, z), fmaf(o[2 * gr][nt][j + 2] * 0x1p20f, down, z),
-                            fmaf(o[2 * gr + 1][nt][j] * 0x1p24f, down, z), fmaf(o[2 * gr + 1][nt][j + 2] * 0x1p20f, down, z));
+                make_float4(fmaf(sum(o[2 * gr][nt], 0), down, z), fmaf(sum(o[2 * gr][nt], 2), down, z),
+                            fmaf(sum(o[2 * gr + 1][nt], 0), down, z), fmaf(sum(o[2 * gr + 1][nt], 2), down, z));
           }
         } else {
 #pragma unroll
@@ -1106,7 +1136,7 @@ struct Shape {
 template <bool INT4, int DK, int DV, int NT, int J>
 constexpr int stages() {
   using H = Shape<INT4, NT, J>;
-  constexpr int room = 227 * 1024 / H::B - 1024 - 1024 - query_smem<INT4, DK, NT>();
+  constexpr int room = 227 * 1024 / H::B - 1024 - 1024 - query_smem<INT4, DK, NT>() - H::W * scale_smem<INT4, DV, H::U>();
   return std::min(INT4 ? 3 : 4, room / (H::W * H::U * Stage<INT4, DK, DV>::kBytes));
 }
 // f of the shape a call's rows take: up to 16 of a head, its queries times its new tokens.  Four at most

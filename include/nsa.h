@@ -465,11 +465,10 @@ NSA_API nsa_status nsa_cache_read(const nsa_cache* cache, const int32_t* seqlens
  *   x = softcap * tanh(x / softcap)         if softcap > 0
  *   x = x + slopes[h] * (u - p)             if slopes (fp32 [h_q] device) is given
  * and softmax over u, in fp32; a query with p < 0 gives zeros.  4-bit keys enter exactly as
- * s (c - 8) + z.  The weights are rounded once before they meet the values: to 16 bits (two bf16
- * terms), or with 4-bit values together with the group's s to f16 (s below 2^-20 of the largest s of that group of dims in
- * the sequence loses digits, below 2^-30 its values count as z - 8 s).  lse (optional, fp32
- * [B, n_new, h_q]): the log of the sum of exp(x), -inf where
- * there is nothing to attend.  Values of tokens that no query of the sequence attends never
+ * s (c - 8) + z.  The weights meet the values as two terms: bf16 (2^-18 of a weight), or with 4-bit values f16 (2^-22, and
+ * down to 2^-32 of the largest weight; an s below 2^-28 of the largest s of that group of dims in the sequence loses digits,
+ * below 2^-36 its values count as z).  Sums are fp32 (values above 2^100 can overflow them).  lse (optional, fp32 [B, n_new,
+ * h_q]): the log of the sum of exp(x), -inf where there is nothing to attend.  Values of tokens that no query of the sequence attends never
  * matter; a NaN or an infinity in an attended value can reach all n_new queries.
  * One launch for short sequences, else two.
  * Workspace: nsa_cache_attention_workspace(cache, args) bytes, 256-byte aligned (0: none is

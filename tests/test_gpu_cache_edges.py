@@ -100,7 +100,7 @@ def key_reach(fmt, q, k):
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (192, 128)])
 @pytest.mark.parametrize("G,n", [(1, 1), (4, 1), (8, 1), (16, 1), (16, 4)])
-@pytest.mark.parametrize("fmt", ["bf16"])
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
 def test_weights_are_exact_far_below_the_outputs_rounding(fmt, dk, dv, G, n):
     """Values that almost cancel under the weights of the (equal) queries, so that the output's own rounding (2^-8 of little)
     hides nothing.  Allowed: weights of two terms, bf16 2^-18 each (2^-16 granted), f16 2^-22; a score's error e twice, with
@@ -132,7 +132,7 @@ def test_weights_are_exact_far_below_the_outputs_rounding(fmt, dk, dv, G, n):
     assert worst <= 1.01, worst
 
 
-@pytest.mark.parametrize("fmt", ["bf16"])
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
 @pytest.mark.parametrize("G,pages", [(1, 1024), (8, 1024), (16, 1024), (16, 1)])
 def test_long_sums_do_not_drift(fmt, G, pages):
     """Equal weights over 60 million tokens (3,200 tiles a warp) whose values cancel exactly: `up` pages of positive values
