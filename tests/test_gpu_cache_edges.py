@@ -176,3 +176,19 @@ def test_long_sums_do_not_drift(fmt, G, pages):
     if pages == 1:
         rounded = 2 ** -15 if up > 1 else 2 ** -20
     assert worst <= rounded + 2 ** -21.4, math.log2(worst)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("G,n", [(1, 1), (4, 1), (8, 1), (16, 1), (2, 2), (8, 3), (16, 2), (16, 4), (16, 16)])
+@pytest.mark.parametrize("cap,sloped,window", [(20.0, True, 70), (0.7, False, 0), (0.0, True, 0)])
+def test_options_in_every_shape(fmt, dk, dv, G, n, cap, sloped, window):
+    """Caps, slopes and windows at once and alone, from one row a head (plain decoding) to 256, over short sequences and over
+    one that is cut over blocks."""
+    h_kv = 2 if G * n < 64 else 1
+    lens = [300, 0, 17, 1200, 1] if G * n < 64 else [75, 900]
+    h_q = h_kv * G
+    slopes = torch.exp2(-8.0 * torch.arange(1, h_q + 1) / h_q) * (1 - 2 * (torch.arange(h_q) % 2)) * 0.05 if sloped else None
+    _, q, held, out, lse, slopes = run_attention(fmt, dk, dv, 16, h_kv, G, lens, n, seed=80 + G, softcap=cap, slopes=slopes,
+                                                 window=window, max_len=2048, max_seqlen=2048)
+    check_attention(out, lse, q, held, lens, softcap=cap, slopes=slopes, window=window)
