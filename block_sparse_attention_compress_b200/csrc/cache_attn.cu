@@ -596,8 +596,9 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           if (NG <= 4) sums[3] = 0u;
           if (NG < 4 && q4 >= NG) sums[0] = sums[1] = sums[2] = 0u;
           if (NG > 4 && q4 + 4 >= NG) sums[1] = sums[3] = last[1] = 0u;
-          // a query that is not finite makes its row NaN
-          if (q4 == 0) sq_sc[nt * 8 + g8] = top >= 0x7f80u ? NAN : fminf(a.scale * pow2(-e2) * 0x1p24f, 1e38f);
+          // a query that is not finite, or so large that its factor leaves fp32, makes its row NaN
+          const float factor = a.scale * pow2(-e2) * 0x1p24f;
+          if (q4 == 0) sq_sc[nt * 8 + g8] = top >= 0x7f80u || !(factor <= 1e38f) ? NAN : factor;
         }
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {

@@ -465,7 +465,7 @@ NSA_API nsa_status nsa_cache_read(const nsa_cache* cache, const int32_t* seqlens
  *   x = softcap * tanh(x / softcap)         if softcap > 0
  *   x = x + slopes[h] * (u - p)             if slopes (fp32 [h_q] device) is given
  * and softmax over u, in fp32; a query with p < 0 gives zeros.  4-bit keys enter exactly as
- * s (c - 8) + z.  The weights meet the values as two terms: bf16 (2^-18 of a weight), or with 4-bit values f16 (2^-22, and
+ * s (c - 8) + z (a query row whose softmax_scale |q| reaches 2^115 can come out as NaN with them).  The weights meet the values as two terms: bf16 (2^-18 of a weight), or with 4-bit values f16 (2^-22, and
  * down to 2^-32 of the largest weight; an s below 2^-28 of the largest s of that group of dims in the sequence loses digits,
  * below 2^-36 its values count as z).  Sums are fp32 (values above 2^100 can overflow them).  lse (optional, fp32 [B, n_new,
  * h_q]): the log of the sum of exp(x), -inf where there is nothing to attend.  Values of tokens that no query of the sequence attends never

@@ -192,3 +192,24 @@ def test_options_in_every_shape(fmt, dk, dv, G, n, cap, sloped, window):
     _, q, held, out, lse, slopes = run_attention(fmt, dk, dv, 16, h_kv, G, lens, n, seed=80 + G, softcap=cap, slopes=slopes,
                                                  window=window, max_len=2048, max_seqlen=2048)
     check_attention(out, lse, q, held, lens, softcap=cap, slopes=slopes, window=window)
+
+
+@pytest.mark.parametrize("size,shows", [(2.0 ** 100, False), (2.0 ** 110, False), (2.0 ** 120, True), (2.0 ** 127, True)])
+def test_the_largest_queries_are_right_or_show(size, shows):
+    """4 bits: the powers of two that take a row of queries into f16 leave fp32 for queries of 2^118 and more (d = 64).  Such a
+    row is NaN, not a finite wrong result, and the other rows stay."""
+    g = gen(90)
+    lens, d = [40], 64
+    k = (torch.randn((40, 1, 2), generator=g).repeat_interleave(32, -1) / size).bfloat16()      # groups without a span: exact
+    v = bf((40, 1, d), g)
+    c = KVCache(1, 40, 1, d, d, fmt="int4", page_size=16, device=DEV)
+    c.append(k.to(DEV), v.to(DEV), i32(lens), cu_seqlens=i32([0, 40]))
+    unit = co.quantise(v.unflatten(-1, (-1, 32)))[1].double().repeat_interleave(32, -1) * 8
+    held = [(co.through_4_bits(k), co.through_4_bits(v), unit)]
+    q = bf((1, 1, 4, d), g)
+    q[0, 0, 1] = (q[0, 0, 1].float() * size / 4).bfloat16()
+    q[0, 0, 1, 0] = size
+    out = c.attend(q.to(DEV), i32(lens), 40)
+    rows = [0, 2, 3] if shows else [0, 1, 2, 3]
+    assert not shows or torch.isnan(out[0, 0, 1].float()).all()
+    check_attention(out[:, :, rows], None, q[:, :, rows], held, lens)
