@@ -48,7 +48,6 @@ namespace nsa {
 namespace {
 
 constexpr int kTile = 16;         // tokens of an MMA's M
-constexpr int kShort = 8, kLonger = 2;   // see the cutting of the work
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -326,7 +325,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   const auto row_of = [](int nt, int column) { return J == 2 ? nt * 8 + column : column >> 1; };
   constexpr int kWarpBytes = warp_smem<INT4, DK, DV, NT, U, S>(), kStep = kTile * U, kQ = query_smem<INT4, DK, NT>();
   extern __shared__ __align__(128) char smem[];
-  __shared__ long long s_scan[2][W];
+  __shared__ long long s_scan[W];
   __shared__ long long s_off;
   __shared__ int s_b, s_h;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g8 = lane >> 2, q4 = lane & 3;
@@ -343,8 +342,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
   // a step of all streams is 1.3 us (4 bits), a part's start and end about 5
   const int extra = 4 * streams;
   int b, h, rt, t = 0;
-  long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles (whole_runs: of the run)
-  bool whole_runs = false;
+  long long left, pos0 = 0, per = 0;   // pos0: index of the first among all tiles
   if (pl.whole) {
     int id = blockIdx.x;
     rt = id % pl.row_tiles; id /= pl.row_tiles;
@@ -361,30 +359,29 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       // a thread with one sequence of one row tile looks its length up once
       const bool single = strip == 1 && pl.row_tiles == 1;
       const int own = single && b0 < b1 ? span_of<kStep>(c, a, pl, b0, 0).tiles : 0;
-      // An item's share of the work: its tiles and, before them, what its start costs in tiles (unit 0); or
-      // its runs of `unit` tiles.  And that of a head, in all row tiles.
-      const auto share = [&](int n, N unit) -> N { return unit == 0 ? n + extra : quotient(n + unit - 1, unit); };
-      const auto units = [&](int bb, int x, N unit) { return share(span_of<kStep>(c, a, pl, bb, x).tiles, unit); };
-      const auto head_units = [&](int bb, N unit) {
-        if (single) return share(own, unit);
+      // An item's share of the work: its tiles and, before them, what its start costs in tiles.  And that of a head, in all
+      // row tiles.
+      const auto units = [&](int bb, int x) -> N { return span_of<kStep>(c, a, pl, bb, x).tiles + extra; };
+      const auto head_units = [&](int bb) {
+        if (single) return (N)(own + extra);
         N w = 0;
-        for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x, unit);
+        for (int x = 0; x < pl.row_tiles; ++x) w += units(bb, x);
         return w;
       };
       // the strips' sums: of those before this thread's, and of all
-      const auto scan = [&](N mine, N& total, long long* warps) {
+      const auto scan = [&](N mine, N& total) {
         N upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
           const N y = __shfl_up_sync(0xffffffffu, upto, d);
           if (lane >= d) upto += y;
         }
-        if (lane == 31) warps[warp] = upto;
+        if (lane == 31) s_scan[warp] = upto;
         __syncthreads();
         total = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const N y = (N)warps[w];
+          const N y = (N)s_scan[w];
           if (w < warp) upto += y;
           total += y;
         }
@@ -392,31 +389,19 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       };
       N mine = 0, total;
       for (int x = b0; x < b1; ++x) {
-        mine += head_units(x, 0) * c.h_kv;
+        mine += head_units(x) * c.h_kv;
         if (blockIdx.x == 0) check_length(c, a, x);
       }
-      N before = scan(mine, total, s_scan[0]), run = max((N)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
-      // Runs that end with their item spare a block the end of one item and the start of the next (about 5 us),
-      // but are longer, since items end inside their last run.  While a run is short, that is the cheaper
-      // cut (64 items of 1100 tokens 15.6 us instead of 18.6); long runs hide those behind the SM's other
-      // blocks, and for a few items finding the runs costs more.
-      const N items = (N)c.batch * c.h_kv * pl.row_tiles, spare = (N)gridDim.x - items;
-      if (spare > 0 && items >= 16 && run <= kShort * streams) {
-        const N longer = max((N)pl.min_tiles, quotient(total + spare - 1, spare));
-        whole_runs = longer <= kShort * streams && longer - run <= kLonger * streams;
-        if (whole_runs) {
-          run = longer;
-          mine = 0;
-          for (int x = b0; x < b1; ++x) mine += head_units(x, run) * c.h_kv;
-          before = scan(mine, total, s_scan[1]);   // in runs: sum over items of ceil(tiles / run) <= spare + items
-        }
-      }
-      const N pos = whole_runs ? (N)blockIdx.x : run * (N)blockIdx.x, unit = whole_runs ? run : 0;
+      // (Runs that end with their items, for many short ones, spare a block the end of one item and the start of the next, but
+      // their ends cost more: 64 items of 1100 tokens in 4 bits, 8 rows, 13.0 us so and 14.4 that way, 64 of 2400 with 16
+      // rows 21.5 and 25.6; of 200 sizes four were quicker that way, by 2 us at most.)
+      const N before = scan(mine, total), run = max((N)pl.min_tiles, quotient(total + gridDim.x - 1, gridDim.x));
+      const N pos = run * (N)blockIdx.x;
       if (pos >= total) return false;
       if (before <= pos && pos < before + mine) {
         N off = pos - before, head;
         int x = b0;
-        for (; off >= (head = head_units(x, unit)) * c.h_kv; ++x) off -= head * c.h_kv;
+        for (; off >= (head = head_units(x)) * c.h_kv; ++x) off -= head * c.h_kv;
         const N skip = quotient(off, head);
         s_b = x;
         s_h = (int)skip;
@@ -428,13 +413,9 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       N at = (N)s_off;
       rt = 0;
       if (pl.row_tiles > 1)
-        for (N n; at >= (n = units(b, rt, unit)); ++rt) at -= n;
+        for (N n; at >= (n = units(b, rt)); ++rt) at -= n;
       t = (int)at;
       left = min(run, (N)(total - pos));
-      if (whole_runs) {
-        t = t * (int)run + extra;
-        left = min(run, (N)(span_of<kStep>(c, a, pl, b, rt).tiles + extra - t));
-      }
       pos0 = pos;
       per = run;
       return true;
@@ -482,7 +463,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     if (first == 0 && take < sp.tiles) {
       cut.b = b;
       cut.head_tile = h * pl.row_tiles + rt;
-      cut.last = whole_runs ? (int)blockIdx.x + runs_before(sp.tiles - 1, per) : runs_before(pos0 - t + extra + sp.tiles - 1, per);
+      cut.last = runs_before(pos0 - t + extra + sp.tiles - 1, per);
       cut.rows = tile_rows;
     }
 
