@@ -151,8 +151,8 @@ __device__ __forceinline__ void put_chunk(const CacheArgs& c, const Row& w, int 
 
 // A block's tokens, looked up by its first threads.
 // kFlight: heads (kReadFlight: units of 16 values) a thread has in flight.  Append with 2 at 4 blocks an SM
-// moves 64K tokens of (64, 4) heads in 622 us (3.44 GB, 5.5 TB/s), with 2 at 3 blocks in 735, with 4 at 2
-// blocks in 749, with 1 at 4 in 722; read with 2 gives back 128K tokens of 4 heads in 92 us, with 4 in 112.
+// moves 64K tokens of (64, 4) heads in 625 us (3.44 GB, 5.5 TB/s), with 2 at 3 blocks in 739, with 4 in 817 (its rows
+// spill), with 1 in 746; read with 2 gives back 128K tokens of 4 heads in 88 us, with 1 in 90, with 4 in 98.
 constexpr int kThreads = 256, kMaxTokens = 16, kFlight = 2, kReadFlight = 2;
 struct Place : Row {
   bool live;   // written (append) or there (read)
@@ -402,7 +402,7 @@ int tokens_per_block(int rows, int most) { return std::max(1, std::min(most, row
 
 template <int DK, int DV>
 cudaError_t append_dims(const CacheArgs& c, const RowsArgs& r, const AppendArgs& a, cudaStream_t st) {
-  // eight; fewer with many heads of values, so that a block is not long in one phase (32 heads: 76 us with four, 79 with eight)
+  // eight; fewer with many heads of values, so that a block is not long in one phase (8K tokens of 32 heads in bf16: 78 us with four, 82 with eight; 64K of 4 in 4 bits: 637 with four, 625 with eight)
   const int n = tokens_per_block(r.rows, std::min(8, 2048 / (c.h_kv * DV / 8))), grid = (r.rows + n - 1) / n;
   if (c.int4) append_kernel<DK, DV, true><<<grid, kThreads, 0, st>>>(c, r, a, n);
   else append_kernel<DK, DV, false><<<grid, kThreads, 0, st>>>(c, r, a, n);
@@ -411,7 +411,7 @@ cudaError_t append_dims(const CacheArgs& c, const RowsArgs& r, const AppendArgs&
 
 template <int DK, int DV>
 cudaError_t read_dims(const CacheArgs& c, const RowsArgs& r, void* k_out, void* v_out, cudaStream_t st) {
-  // about four units a thread: 12 tokens of 4 heads (128K of them 87 us; 6 tokens 96), 2 of 32 (16K: 62; 8 tokens 70)
+  // about four units a thread: 12 tokens of 4 heads (128K of them 88 us; 6 tokens 96), 2 of 32 (16K: 64; 8 tokens 70)
   const int n = tokens_per_block(r.rows, std::min(kMaxTokens, 1024 / (c.h_kv * (DK + DV) / 16))), grid = (r.rows + n - 1) / n;
   uint4 *k = static_cast<uint4*>(k_out), *v = static_cast<uint4*>(v_out);
   if (c.int4) read_kernel<DK, DV, true><<<grid, kThreads, 0, st>>>(c, r, k, v, n);

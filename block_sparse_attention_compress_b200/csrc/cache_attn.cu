@@ -15,7 +15,7 @@
 // c 2^-20, which the tensor cores multiply exactly: no conversion.  The queries of the latter are
 // divided by 16, and every query row is scaled by a power of two so that f16 holds it.  (The e4m3
 // MMA would take the nibbles as they are too, but on sm_100 it is carried out as conversions and
-// 16-bit MMAs: 781 us instead of 571 for 32 sequences of 64K tokens.)  A group's (s, z) come in behind
+// 16-bit MMAs: 781 us instead of 571 for 32 sequences of 64K tokens in the kernel's first form.)  A group's (s, z) come in behind
 // the product: S = sum_g s_g (sum c q) + (z_g - 8 s_g) sum_g q, the second sum as more MMAs with
 // the stored pairs as A and the groups' query sums (three bf16 terms: 24 bits) as B.
 //
@@ -190,7 +190,7 @@ struct Span {
   int p0, lo, hi, base, tiles;
 };
 template <int STEP>
-__device__ __forceinline__ Span span_of(const CacheArgs& c, const CacheAttnArgs& a, const Plan& p, int b, int rt) {
+__device__ __forceinline__ Span span_of(const CacheAttnArgs& a, const Plan& p, int b, int rt) {
   Span s;
   s.p0 = min(max(__ldg(a.seqlens + b), 0), a.max_seqlen) - a.n_new;
   s.hi = max(0, s.p0 + p.last[rt] + 1);
@@ -348,7 +348,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
     rt = id % pl.row_tiles; id /= pl.row_tiles;
     h = id % c.h_kv;
     b = id / c.h_kv;
-    left = (long long)span_of<kStep>(c, a, pl, b, rt).tiles + extra;
+    left = (long long)span_of<kStep>(a, pl, b, rt).tiles + extra;
     if (h == 0 && rt == 0 && threadIdx.x == 0) check_length(c, a, b);
   } else {
     const auto cut_work = [&](auto zero) {   // false: nothing is left for this block
@@ -358,10 +358,10 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       const int b0 = min(c.batch, (int)threadIdx.x * strip), b1 = min(c.batch, b0 + strip);
       // a thread with one sequence of one row tile looks its length up once
       const bool single = strip == 1 && pl.row_tiles == 1;
-      const int own = single && b0 < b1 ? span_of<kStep>(c, a, pl, b0, 0).tiles : 0;
+      const int own = single && b0 < b1 ? span_of<kStep>(a, pl, b0, 0).tiles : 0;
       // An item's share of the work: its tiles and, before them, what its start costs in tiles.  And that of a head, in all
       // row tiles.
-      const auto units = [&](int bb, int x) -> N { return span_of<kStep>(c, a, pl, bb, x).tiles + extra; };
+      const auto units = [&](int bb, int x) -> N { return span_of<kStep>(a, pl, bb, x).tiles + extra; };
       const auto head_units = [&](int bb) {
         if (single) return (N)(own + extra);
         N w = 0;
@@ -428,7 +428,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
 
   Cut cut{0, 0, -1, 0};
   while (left > 0) {
-    const Span sp = span_of<kStep>(c, a, pl, b, rt);
+    const Span sp = span_of<kStep>(a, pl, b, rt);
     // the block's part of the item's share, [t, t + part), and its tiles in that
     const int part = (int)min(left, (long long)(sp.tiles + extra - t)), first = max(0, t - extra);
     const int take = max(0, t + part - extra) - first;
@@ -498,7 +498,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       const long long next = (long long)(cp_j + 1) * c.page_size;
       ahead = next < min(sp.hi, cp_end) ? __ldg(pages + cp_j + 1) : -1;
     };
-    if (ta < tb && sp.hi > 0) {
+    if (ta < tb) {
       cp_j = cp_u / c.page_size;
       cp_off = cp_u - cp_j * c.page_size;
       open_page(__ldg(pages + cp_j));
@@ -1103,9 +1103,10 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
   if (a.lse && lane == 0) a.lse[row] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }
 
-// Warps per block, blocks per SM, tiles of 16 tokens per step.  4 bits: eight warps an SM with all the registers
-// they ask for; twelve of 168 spill (16 rows, 8 x 64K tokens: 175 us instead of 147), and one tile a step leaves a
-// warp too little that is independent (155).  bf16: the ring needs the shared memory.
+// Warps per block, blocks per SM, tiles of 16 tokens per step.  4 bits: eight warps an SM of up to 255 registers (with 16
+// rows and (128, 128) or (192, 128) 31 to 45 words of a thread spill, in bf16 20 to 33); twelve of 168 spill far more (16
+// rows, 8 x 64K tokens: 208 us instead of 157), and one tile a step leaves a warp too little that is independent (169).
+// bf16: the ring needs the shared memory.
 template <bool INT4, int NT, int J>
 struct Shape {
   static constexpr bool kInt4 = INT4;
@@ -1122,7 +1123,7 @@ constexpr int stages() {
   return std::min(INT4 ? 3 : 4, room / (H::W * H::U * Stage<INT4, DK, DV>::kBytes));
 }
 // f of the shape a call's rows take: up to 16 of a head, its queries times its new tokens.  Four at most
-// use one of a lane's columns (4 bits, 32 heads of one query over 64K tokens: 86 us instead of 97); a bf16
+// use one of a lane's columns (4 bits, 32 heads of one query over 64K tokens: 93 us instead of 99); a bf16
 // cache waits for memory either way.
 template <class F>
 auto with_shape(bool int4, int rows, F f) {
@@ -1131,8 +1132,11 @@ auto with_shape(bool int4, int rows, F f) {
 }
 
 constexpr int kSms = 148;
-// A warp's share of items that are not cut: the second kernel costs 5 us, so does a share of 128 tokens
-constexpr int kWholeTokens = 128;
+// A warp's share of items that are not cut: the second kernel and the parts cost 2 to 5 us, so does a share of 128 tokens
+// (8 rows, 32 items of 500 tokens: whole 7.5 us in bf16 and 9.1 in 4 bits, cut 9.2 and 10.8; of twice that, 13.0 and 13.4
+// against 10.5 and 11.2).  Twice as much where the items alone fill the SMs, from 64 on: there it is about even (1,500
+// tokens in bf16 13.1 and 13.0, 1,000 in 4 bits 13.6 and 12.8), at 128 items 14.4 against 19.1 and 13.9 against 17.6.
+constexpr int kWholeTokens = 128, kManyItems = 64;
 
 Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   Plan p{};
@@ -1153,7 +1157,7 @@ Plan plan_of(const CacheArgs& c, const CacheAttnArgs& a) {
   const long long tiles = (range + step - 1) / step, items = (long long)c.batch * c.h_kv * p.row_tiles;
   p.min_tiles = 2 * (W / p.row_groups);
   p.small = items * (tiles + 4 * W) < (1 << 30);
-  p.whole = range <= kWholeTokens * (W / p.row_groups) * (items >= 64 ? 2 : 1);
+  p.whole = range <= kWholeTokens * (W / p.row_groups) * (items >= kManyItems ? 2 : 1);
   const long long most = (long long)kSms * resident;
   // items <= 2^31 (cache_attn_fits), tiles <= 2^26
   p.blocks = (int)(p.whole ? std::min<long long>(items, INT32_MAX) : std::min(most, (items * tiles + p.min_tiles - 1) / p.min_tiles));
