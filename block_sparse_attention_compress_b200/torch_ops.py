@@ -239,7 +239,7 @@ class KVCache:
         """Memory for `stream`: from that stream's pool, since a block of another's may still be in use there."""
         if stream is not None:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=self.device)
+                stream = torch.cuda.ExternalStream(stream if stream != 1 else 0, device=self.device)   # 1: the default stream's handle
             with torch.cuda.stream(stream):
                 return like.new_empty(shape, dtype=dtype)
         if like.shape == shape and dtype is like.dtype:   # the quickest of torch's ways

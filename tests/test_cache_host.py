@@ -273,6 +273,21 @@ def test_calls_by_addresses_run_on_the_current_stream(monkeypatch):
         assert streams[-3:] == [want] * 3
 
 
+def test_the_default_streams_own_handle_is_the_default_stream(monkeypatch):
+    """cudaStreamLegacy is 1, which torch would take for a stream of its own pool."""
+    import contextlib
+
+    from block_sparse_attention_compress_b200.torch_ops import KVCache
+    handles = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handles.append(handle))
+    cache = KVCache.__new__(KVCache)
+    cache.device = torch.device("cpu")
+    for handle in (1, 0, 2, 0x7f00):
+        cache._new(torch.zeros(3), (4,), handle)
+    assert handles == [0, 0, 2, 0x7f00]
+
+
 # ------------------------------------------------------------------ the oracle's pins
 
 def test_rotation_turns_pairs_by_the_angle():
