@@ -442,7 +442,8 @@ NSA_API nsa_status nsa_cache_append(const nsa_cache* cache, const nsa_cache_appe
 
 /*
  * nsa_cache_read -- the last tokens of every sequence out of the cache, as contiguous bf16 keys and
- * values (for nsa_compress, a prompt that continues a cached prefix, or a check).  Rows as for
+ * values (for nsa_compress, whose blocks then serve nsa_decode, or a check; no call here attends
+ * from a prompt's rows to a longer history).  Rows as for
  * nsa_cache_append: n_new per sequence into k_out [B, n_new, h_kv, d_k], v_out [B, n_new, h_kv, d_v],
  * or packed by cu_seqlens into [total_tokens, h_kv, d].  4-bit values are s (c - 8) + z rounded once
  * to bf16.  Rows before position 0 and rows whose page is out of range come out as zeros; rows
@@ -469,7 +470,7 @@ NSA_API nsa_status nsa_cache_read(const nsa_cache* cache, const int32_t* seqlens
  * down to 2^-32 of the largest weight; an s below 2^-28 of the largest s of that group of dims in the sequence loses digits,
  * below 2^-36 its values count as z).  Sums are fp32 (values above 2^100 can overflow them).  lse (optional, fp32 [B, n_new,
  * h_q]): the log of the sum of exp(x), -inf where there is nothing to attend.  Values of tokens that no query of the sequence attends never
- * matter; a NaN or an infinity in an attended value can reach all n_new queries.
+ * matter; a NaN or an infinity in an attended value comes out as NaN and can reach all n_new queries.
  * One launch for short sequences, else two.
  * Workspace: nsa_cache_attention_workspace(cache, args) bytes, 256-byte aligned (0: none is
  * needed); nothing in it has to be set before or kept after the call.  Results do not depend on the
