@@ -296,6 +296,34 @@ struct Walk {
   }
 };
 
+// Zeros for the tokens of a step with a value that is not finite (4 bits: a scale or an offset): their bits
+template <class T, bool INT4, int DV, int U>
+__device__ __forceinline__ uint32_t drop_odd_values(char* step, int lane) {
+  const auto odd2 = [](uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; };
+  // tokens of a step, lanes of a token, and bytes of a lane
+  constexpr int kTokens = U * kTile, kLanes = 32 / kTokens, kRow = INT4 ? T::kRowVs : T::kRowV, kBytes = kRow / kLanes;
+  const int tok = lane / kLanes;
+  char* row = step + tok / kTile * T::kBytes + (INT4 ? T::kVs : T::kV) + tok % kTile * kRow + lane % kLanes * kBytes;
+  bool odd = false;
+#pragma unroll 1
+  for (int i = 0; i < kBytes; i += 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + i);
+    odd |= odd2(w.x) || odd2(w.y);
+  }
+  uint32_t lanes = __ballot_sync(0xffffffffu, odd), tokens = lanes;
+  if (lanes == 0) return 0;
+  if constexpr (kLanes == 2) {
+    tokens = 0;
+    for (int i = 0; i < kTokens; ++i) tokens |= (lanes >> (2 * i) & 3u) ? 1u << i : 0u;
+  }
+  if (tokens >> tok & 1) {
+#pragma unroll 1
+    for (int i = 0; i < kBytes; i += 8) *reinterpret_cast<uint2*>(row + i) = make_uint2(0, 0);
+  }
+  __syncwarp();
+  return tokens;
+}
+
 // Shared memory of a block: a ring (and later the joined rows) per warp, then in 4 bits the queries of
 // each row group: per tile of 8 rows the B fragments [DK / 32][32 lanes] x 16 bytes, the group sums'
 // [32 lanes] x (16 + 8) bytes and the rows' factors.
@@ -653,7 +681,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
       __syncwarp();
       const uint32_t gone = missing >> (stage * U) & ((1u << U) - 1);
       copy_next(stage == 0 ? S - 1 : stage - 1);
-      const char* st = ring + stage * U * T::kBytes;
+      char* st = ring + stage * U * T::kBytes;
       stage = stage == S - 1 ? 0 : stage + 1;
       const int u0 = sp.base + tile * kStep;
 
@@ -732,6 +760,34 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
           }
       }
 
+      // ---- a value that is not finite, in a step that some rows see more of than others: no MMA may meet it, since 0 times it
+      // is a NaN.  Zeros take its token's place, and the rows that attend the token are NaN from here on
+      const bool edge = gone || u0 < all_lo || u0 + kStep > all_hi;
+      if (edge && pl.first[rt] != pl.last[rt]) {
+        if (const uint32_t odd = drop_odd_values<T, INT4, DV, U>(st, lane)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              bool met = false;
+              for (uint32_t left_odd = odd; left_odd; left_odd &= left_odd - 1) {
+                const int u = u0 + __ffs(left_odd) - 1, p = pos[nt][j];
+                met |= u <= p && !(a.window > 0 && u <= p - a.window);
+              }
+              const float spoil = met ? NAN : 0.f;
+              if constexpr (INT4) {
+#pragma unroll
+                for (int gr = 0; gr < NH; ++gr) zacc[nt][gr][j] += spoil;
+              } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                  for (int e = j; e < 4; e += 2) o[mt][nt][e] += spoil;
+              }
+            }
+        }
+      }
+
       // ---- softmax: scores in log2 units, the reference moved only when a score passes it by 8
       uint32_t sv[INT4 ? NH : 1];   // 4 bits: the scales of the values of token `lane` of the step
       bool move = false;
@@ -754,7 +810,7 @@ cache_attn_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, Cut* 
             }
             s[x][nt][e] = y;
           }
-      if (gone || u0 < all_lo || u0 + kStep > all_hi) {
+      if (edge) {
 #pragma unroll
         for (int x = 0; x < U; ++x)
 #pragma unroll
@@ -1104,7 +1160,7 @@ cache_join_kernel(const CacheArgs c, const CacheAttnArgs a, const Plan pl, const
 }
 
 // Warps per block, blocks per SM, tiles of 16 tokens per step.  4 bits: eight warps an SM of up to 255 registers (with 16
-// rows and (128, 128) or (192, 128) 31 to 45 words of a thread spill, in bf16 20 to 33); twelve of 168 spill far more (16
+// rows and (128, 128) or (192, 128) 32 to 47 words of a thread spill, in bf16 18 to 45); twelve of 168 spill far more (16
 // rows, 8 x 64K tokens: 208 us instead of 157), and one tile a step leaves a warp too little that is independent (169).
 // bf16: the ring needs the shared memory.
 template <bool INT4, int NT, int J>

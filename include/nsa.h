@@ -469,8 +469,8 @@ NSA_API nsa_status nsa_cache_read(const nsa_cache* cache, const int32_t* seqlens
  * s (c - 8) + z (a query row whose softmax_scale |q| reaches 2^115 can come out as NaN with them).  The weights meet the values as two terms: bf16 (2^-18 of a weight), or with 4-bit values f16 (2^-22, and
  * down to 2^-32 of the largest weight; an s below 2^-28 of the largest s of that group of dims in the sequence loses digits,
  * below 2^-36 its values count as z).  Sums are fp32 (values above 2^100 can overflow them).  lse (optional, fp32 [B, n_new,
- * h_q]): the log of the sum of exp(x), -inf where there is nothing to attend.  Values of tokens that no query of the sequence attends never
- * matter; a NaN or an infinity in an attended value comes out as NaN and can reach all n_new queries.
+ * h_q]): the log of the sum of exp(x), -inf where there is nothing to attend.  Values of tokens that a query does not attend never
+ * matter to it; a NaN or an infinity in an attended value comes out as one or the other, in its dim or group of dims at least.
  * One launch for short sequences, else two.
  * Workspace: nsa_cache_attention_workspace(cache, args) bytes, 256-byte aligned (0: none is
  * needed); nothing in it has to be set before or kept after the call.  Results do not depend on the

@@ -213,3 +213,39 @@ def test_the_largest_queries_are_right_or_show(size, shows):
     rows = [0, 2, 3] if shows else [0, 1, 2, 3]
     assert not shows or torch.isnan(out[0, 0, 1].float()).all()
     check_attention(out[:, :, rows], None, q[:, :, rows], held, lens)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+@pytest.mark.parametrize("odd", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dk,dv,G,n,window", [(64, 64, 1, 4, 0), (128, 128, 2, 4, 50), (192, 128, 4, 4, 50), (128, 128, 8, 5, 0),
+                                              (64, 64, 16, 4, 20), (128, 128, 16, 16, 100)])
+def test_odd_values_reach_the_queries_that_attend_them_alone(fmt, odd, dk, dv, G, n, window):
+    """A NaN or an infinity in a draft's value leaves the drafts before it alone, and one that has left a query's window that
+    query; all that attend it show it."""
+    lens = [700, n, 90]
+    h_kv, h_q = 2, 2 * G
+    c, q, _, want, want_lse, _ = run_attention(fmt, dk, dv, 16, h_kv, G, lens, n, seed=95, window=window)
+    for b, i in ((0, n - 2), (2, 1), (1, n - 1), (0, 0)):           # the position of query i of sequence b
+        where = lens[b] - n + i
+        places = [where] if not window else [where, where - window + 1]
+        for u in places:
+            if u < 0:
+                continue
+            page, off = int(c.page_table[b, u // 16]), u % 16
+            pool = c.v if fmt == "bf16" else c.v_scale
+            at = (page, off, 1) if fmt == "bf16" else (page, 1, off)
+            kept = pool[at].clone()
+            pool[at + ((dv - 3,) if fmt == "bf16" else (dv // 32 - 1, 1))] = odd
+            lse = torch.full_like(want_lse, 7.0)
+            out = c.attend(q, i32(lens), max(lens), window=window, lse=lse)
+            pool[at] = kept
+            meets = torch.zeros((len(lens), n, h_q), dtype=torch.bool)
+            for j in range(n):
+                p = lens[b] - n + j
+                if u <= p and (not window or u > p - window):
+                    meets[b, j, G:] = True
+            got = ~torch.isfinite(out.float()).all(-1).cpu()     # an infinity times a weight is one, or NaN with its second term
+            assert torch.equal(got, meets), (b, i, u)
+            assert torch.equal(out[~meets.to(DEV)], want[~meets.to(DEV)])
+            assert torch.equal(lse, want_lse)
+    assert c.device_status() == 0
