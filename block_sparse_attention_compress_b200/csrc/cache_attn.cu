@@ -9,7 +9,8 @@
 //                             P^T's B fragment by movmatrix.
 // The operands come from registers (warp-level MMA): in 4 bits a tcgen05 form would have to write
 // every widened value to shared memory and read it back, 640 bytes a token against the 200 that
-// are stored, about 210 cycles of an SM's shared memory for 16 tokens of (192, 128); HBM takes 120.
+// are stored, about 210 cycles of an SM's shared memory for 16 tokens of (192, 128); HBM takes 120.  In bf16 that reason holds
+// up to 16 rows a head, where HBM bounds the call; more rows read each tile again (64 rows: 275 us where HBM takes 84).
 //
 // Keys in 4 bits: w & 0x000f000f and w & 0x00f000f0 are pairs of f16 subnormals c 2^-24 and
 // c 2^-20, which the tensor cores multiply exactly: no conversion.  The queries of the latter are
@@ -36,7 +37,7 @@
 // leaves a part in each block's slots and a second small kernel joins the parts by their maxima and
 // sums, in a fixed order.
 //
-// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 215-231 us, 5.8-6.2 TB/s.  32 x 64K tokens
+// Measured (B200): 32 x 16K tokens in bf16, 64 query heads on 4, (192, 128): 225-232 us, 5.8-6.0 TB/s.  32 x 64K tokens
 // in 4 bits, same heads: 579 us, 2.9 TB/s; 32 heads of one query over 128K tokens in 4 bits, (128, 128): 171 us, 3.9
 // TB/s.  In 4 bits the issue slots bound it, not HBM: logic at half rate, MMAs and fp32 products compete for the same
 // slots (4 MMAs, 16 logic and 16 fma instructions take 58 cycles, not 32).
